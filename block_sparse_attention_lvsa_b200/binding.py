@@ -35,9 +35,17 @@ BSA_OP_BLOCKSPARSE_FWD = 1
 BSA_OP_DENSE_BLOCKMASS = 2
 BSA_OP_BLOCKMASS = 3
 
+BSA_BF16 = 0
+BSA_F16 = 1
+BSA_F32 = 2
+BSA_ROPE_ADJACENT = 0
+BSA_ROPE_SPLIT = 1
+
 EXPORTED = ("lvsa_build_index", "lvsa_build_index_window", "attn_dense_blockmass", "attn_blockmass", "losa_select", "blocksparse_attn_fwd",
             "bsa_workspace_bytes", "bsa_get_device_status", "bsa_status_string",
-            "bsa_debug_expired_wait", "bsa_version", "blocksparse_attn_fwd_noalloc")
+            "bsa_debug_expired_wait", "bsa_version", "blocksparse_attn_fwd_noalloc",
+            "rope_build_table", "rope_apply", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+            "qk_norm_rope_bwd_workspace_bytes")
 
 
 class BsaError(RuntimeError):
@@ -62,6 +70,29 @@ class bsa_index(ctypes.Structure):
     ]
 
 
+class bsa_heads(ctypes.Structure):
+    """Mirror of ``struct bsa_heads`` in include/bsa.h."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("H", ctypes.c_int),
+        ("token_stride", ctypes.c_longlong),
+        ("head_stride", ctypes.c_longlong),
+    ]
+
+
+class bsa_rope(ctypes.Structure):
+    """Mirror of ``struct bsa_rope`` in include/bsa.h."""
+    _fields_ = [
+        ("pairing", ctypes.c_int),
+        ("pairs", ctypes.c_int * 3),
+        ("len", ctypes.c_int * 3),
+        ("table", ctypes.c_void_p * 3),
+        ("grid", ctypes.c_int * 3),
+        ("first", ctypes.c_int * 3),
+        ("pos", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -69,6 +100,7 @@ def _load():
             "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, D, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_float, ctypes.c_size_t
+    L, HP, RP = ctypes.c_longlong, ctypes.POINTER(bsa_heads), ctypes.POINTER(bsa_rope)
     sig = {
         "lvsa_build_index": (I, [I, I, I, I, I, P, P, P]),
         "lvsa_build_index_window": (I, [I, I, I, I, P, P, P]),
@@ -82,6 +114,11 @@ def _load():
         "bsa_debug_expired_wait": (I, [ctypes.c_longlong, I, P]),
         "bsa_version": (ctypes.c_char_p, []),
         "blocksparse_attn_fwd_noalloc": (I, [P, P, P, I, I, I, F, ctypes.POINTER(bsa_index), P, P, P]),
+        "rope_build_table": (I, [I, I, D, D, D, P, P]),
+        "rope_apply": (I, [HP, HP, I, L, I, RP, I, P]),
+        "qk_norm_rope_fwd": (I, [HP, HP, HP, HP, I, L, I, P, P, I, F, RP, P]),
+        "qk_norm_rope_bwd": (I, [HP, HP, HP, HP, HP, HP, I, L, I, P, P, I, F, RP, P, P, P, SZ, P]),
+        "qk_norm_rope_bwd_workspace_bytes": (SZ, [L, I, I, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -363,6 +400,232 @@ def losa_select(mass: torch.Tensor, tau: float = 0.99, idx=None, cnt=None, strea
     rc = _lib.losa_select(_ptr(mass), H, nQB, nKB, float(tau), _ptr(idx), _ptr(cnt), _stream(stream))
     _check("losa_select", rc)
     return idx, cnt
+
+
+# ------------------------------------------- rotary positions, normed q and k ---
+_DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16, torch.float32: BSA_F32}
+_PAIRINGS = {"adjacent": BSA_ROPE_ADJACENT, "split": BSA_ROPE_SPLIT}
+
+
+class _on_device:
+    """Makes the tensors' device current for a call and says which stream it
+    goes to; what the call allocates comes from that stream's pool, so that it
+    is not handed to other work while the call still uses it."""
+
+    def __init__(self, device: torch.device, stream):
+        self._guard = None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self._guard = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None, heads: Optional[int] = None) -> bsa_heads:
+    """bsa_heads of a CUDA tensor [N, H, d] with unit channel stride (of the
+    type, device and sizes of ``like``; H may be given apart)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor of shape [N, H, d]")
+    N, H, d = t.shape
+    if like is not None:
+        shape = (like.shape[0], like.shape[1] if heads is None else heads, like.shape[2])
+        if (N, H, d) != shape or t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name} must be {like.dtype} of shape {shape} on {like.device}, "
+                             f"got {t.dtype} {(N, H, d)} on {t.device}")
+    ts, hs, cs = t.stride()
+    if cs != 1 and d > 1:
+        raise ValueError(f"{name} must have unit channel stride")
+    return bsa_heads(t.data_ptr(), H, ts if N > 1 else 0, hs if H > 1 else 0)
+
+
+def _weight(name: str, w: Optional[torch.Tensor], x: torch.Tensor) -> None:
+    if w is None:
+        return
+    if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"{name} must be float32 or {x.dtype}")
+    _check_tensor(name, w, (x.shape[2],), w.dtype, x.device)
+
+
+def _weight_type(wq, wk, x) -> int:
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError("wq and wk must have the same dtype")
+    w = wq if wq is not None else wk
+    return BSA_F32 if w is None else _DTYPES[w.dtype]
+
+
+def _rope_for(rope: Optional[bsa_rope], x: torch.Tensor):
+    """The tables and positions are read by pointer: they must be on x's device and hold x's tokens."""
+    if rope is None:
+        return None
+    if not isinstance(rope, bsa_rope):
+        raise ValueError("rope must come from rope_axes")
+    if rope._device != x.device:
+        raise ValueError(f"the rotation's tables are on {rope._device}, the tensor on {x.device}")
+    if rope._pos is not None and rope._pos.shape[0] != x.shape[0]:
+        raise ValueError(f"pos holds {rope._pos.shape[0]} tokens, the tensor {x.shape[0]}")
+    return ctypes.byref(rope)
+
+
+def rope_build_table(length: int, pairs: int, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
+                     table: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
+    """cos and sin of one axis, float32 [length, pairs, 2]: row i, pair j holds the
+    angle (start + i * step) * theta ** (-j / pairs)."""
+    if length < 1 or pairs < 1:
+        raise ValueError("length and pairs must be at least 1")
+    if table is not None:
+        device = table.device
+        _check_tensor("table", table, (length, pairs, 2), torch.float32, device)
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("the table must be on a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on_device(device, stream) as st:
+        if table is None:
+            table = torch.empty((length, pairs, 2), dtype=torch.float32, device=device)
+        rc = _lib.rope_build_table(length, pairs, float(theta), float(start), float(step), _ptr(table), st)
+    _check("rope_build_table", rc)
+    return table
+
+
+def rope_axes(tables, grid=None, first=(0, 0, 0), pos: Optional[torch.Tensor] = None,
+              pairing: str = "adjacent") -> bsa_rope:
+    """Rotary positions over up to three axes, for rope_apply and qk_norm_rope_*.
+
+    ``tables``: one float32 [len, pairs, 2] per axis (rope_build_table), the
+    outermost axis (time) first.  Either ``grid`` gives the extent of every
+    axis (tokens row-major, starting at ``first``; tokens behind the grid are
+    not turned), or ``pos`` (int32 [N, 3]) lists the positions (negative: not
+    turned along that axis).  ``pairing``: "adjacent" channels 2j, 2j+1 or
+    "split" channels j, j+d/2 form a pair."""
+    tables = list(tables)
+    if not 1 <= len(tables) <= 3:
+        raise ValueError("rope_axes takes one to three tables")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}")
+    if (grid is None) == (pos is None):
+        raise ValueError("give either grid or pos")
+    r = bsa_rope()
+    r.pairing = _PAIRINGS[pairing]
+    dev = None
+    for a, t in enumerate(tables):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_cuda:
+            raise ValueError("a table must be a float32 CUDA tensor [len, pairs, 2]")
+        dev = t.device if dev is None else dev
+        _check_tensor("table", t, (t.shape[0], t.shape[1], 2), torch.float32, dev)
+        r.pairs[a], r.len[a], r.table[a] = t.shape[1], t.shape[0], t.data_ptr()
+    if pos is not None:
+        _check_tensor("pos", pos, (pos.shape[0], 3), torch.int32, dev)
+        r.pos = pos.data_ptr()
+    else:
+        grid, first = tuple(grid), tuple(first)
+        if len(grid) != len(tables) or len(first) < len(grid):
+            raise ValueError("grid and first must give every axis")
+        for a in range(3):
+            r.grid[a] = grid[a] if a < len(grid) else 1
+            r.first[a] = first[a] if a < len(grid) else 0
+    r._device, r._pos = dev, pos
+    r._tensors = (tables, pos)             # the struct holds raw pointers: keep the tensors alive with it
+    return r
+
+
+def rope_apply(x: torch.Tensor, rope: bsa_rope, inverse: bool = False, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """x [N, H, d] turned by its tokens' positions (``inverse``: turned back, which is
+    also the gradient).  ``out`` may be x itself; x may be a strided slice."""
+    hx = _heads("x", x)
+    rp = _rope_for(rope, x)
+    if rp is None:
+        raise ValueError("rope must come from rope_axes")
+    N, H, d = x.shape
+    with _on_device(x.device, stream) as st:
+        if out is None:
+            out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
+        rc = _lib.rope_apply(ctypes.byref(hx), ctypes.byref(_heads("out", out, x)), _DTYPES[x.dtype], N, d, rp,
+                             int(bool(inverse)), st)
+    _check("rope_apply", rc)
+    return out
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: Optional[torch.Tensor] = None,
+                     wk: Optional[torch.Tensor] = None, rope: Optional[bsa_rope] = None, eps: float = 1e-6,
+                     qo: Optional[torch.Tensor] = None, ko: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of every head of q [N, Hq, d] and k [N, Hk, d] (weights wq, wk [d] or
+    None), then the rotation (None: none), in one pass; returns (qo, ko).  k may be
+    None (then ko is).  An output may be its own input."""
+    hq = _heads("q", q)
+    hk = None if k is None else _heads("k", k, q, k.shape[1] if k.dim() == 3 else None)
+    if k is None and (wk is not None or ko is not None):
+        raise ValueError("wk and ko need k")
+    _weight("wq", wq, q)
+    _weight("wk", wk, q)
+    wtype = _weight_type(wq, wk, q)
+    rp = _rope_for(rope, q)
+    N, _, d = q.shape
+    with _on_device(q.device, stream) as st:
+        if qo is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if ko is None and k is not None:
+            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        ho = _heads("qo", qo, q)
+        hko = None if k is None else _heads("ko", ko, k)
+        rc = _lib.qk_norm_rope_fwd(ctypes.byref(hq), None if k is None else ctypes.byref(hk), ctypes.byref(ho),
+                                   None if k is None else ctypes.byref(hko), _DTYPES[q.dtype], N, d, _ptr(wq),
+                                   _ptr(wk), wtype, float(eps), rp, st)
+    _check("qk_norm_rope_fwd", rc)
+    return qo, ko
+
+
+def qk_norm_rope_bwd(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+                     wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+                     rope: Optional[bsa_rope] = None, eps: float = 1e-6, dq: Optional[torch.Tensor] = None,
+                     dk: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of qk_norm_rope_fwd: (dq, dk, dwq, dwk) for the output gradients gq, gk.
+    dwq and dwk are float32 [d], None where the weight is None; dk is None where k is."""
+    hq = _heads("q", q)
+    hgq = _heads("gq", gq, q)
+    if (gk is None) != (k is None) or (k is None and (wk is not None or dk is not None)):
+        raise ValueError("gk, wk and dk need k, and k needs gk")
+    hk = None if k is None else _heads("k", k, q, k.shape[1] if k.dim() == 3 else None)
+    hgk = None if k is None else _heads("gk", gk, k)
+    _weight("wq", wq, q)
+    _weight("wk", wk, q)
+    wtype = _weight_type(wq, wk, q)
+    rp = _rope_for(rope, q)
+    _check_workspace(workspace, q.device)
+    N, H, d = q.shape
+    need = int(_lib.qk_norm_rope_bwd_workspace_bytes(N, H, 0 if k is None else k.shape[1], d))
+    if need == ctypes.c_size_t(-1).value:
+        raise BsaError("qk_norm_rope_bwd_workspace_bytes", BSA_ERR_ARG)
+    with _on_device(q.device, stream) as st:
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None and k is not None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        dwq = None if wq is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        dwk = None if wk is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        hdq = _heads("dq", dq, q)
+        hdk = None if k is None else _heads("dk", dk, k)
+        opt = lambda h: None if h is None else ctypes.byref(h)      # noqa: E731
+        rc = _lib.qk_norm_rope_bwd(opt(hgq), opt(hgk), opt(hq), opt(hk), opt(hdq), opt(hdk), _DTYPES[q.dtype], N, d,
+                                   _ptr(wq), _ptr(wk), wtype, float(eps), rp, _ptr(dwq), _ptr(dwk), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), st)
+    _check("qk_norm_rope_bwd", rc)
+    return dq, dk, dwq, dwk
 
 
 def get_device_status(stream=None) -> int:

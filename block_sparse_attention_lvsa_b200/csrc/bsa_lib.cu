@@ -17,6 +17,7 @@
 #include "losa_select.cuh"
 #include "attn_fwd.cuh"
 #include "blockmass.cuh"
+#include "rope.cuh"
 
 namespace {
 
@@ -453,3 +454,260 @@ extern "C" int blocksparse_attn_fwd_noalloc(const void* q, const void* k, const 
   }
   return blocksparse_attn_fwd(q, k, v, N, H, d, scale, index, o, lse, scratch, kNoAllocScratchBytes, stream);
 }
+
+// ---------------------------------------------------------------------------
+// Rotary positions and the normed rotation of queries and keys.
+namespace {
+
+int esize(int dtype) { return dtype == BSA_F32 ? 4 : 2; }
+
+// rows of an output tensor must not overlap
+bool rows_apart(const bsa_heads* t, long long N, int d) {
+  const long long lo = std::min(t->token_stride, t->head_stride), hi = std::max(t->token_stride, t->head_stride);
+  if (N == 1) return t->H == 1 || t->head_stride >= d;
+  if (t->H == 1) return t->token_stride >= d;
+  const long long inner = t->token_stride < t->head_stride ? N : t->H;
+  return lo >= d && hi / lo >= inner;
+}
+
+int check_heads(const bsa_heads* t, int dtype, long long N, int d, bool out) {
+  if (!t || !t->data || t->H < 1 || t->H > 65535 || t->token_stride < 0 || t->head_stride < 0) return BSA_ERR_ARG;
+  const size_t es = esize(dtype);
+  if (!aligned(t->data, 16) || (t->token_stride * es) % 16 || (t->head_stride * es) % 16) return BSA_ERR_ARG;
+  // byte offsets stay far below 2^63
+  if (t->token_stride > (1LL << 60) / N || t->head_stride > (1LL << 60) / t->H) return BSA_ERR_UNSUPPORTED;
+  if (out && !rows_apart(t, N, d)) return BSA_ERR_ARG;
+  return BSA_OK;
+}
+
+int check_sizes(int dtype, long long N, int d) {
+  if (dtype != BSA_BF16 && dtype != BSA_F16 && dtype != BSA_F32) return BSA_ERR_ARG;
+  if (N < 1) return BSA_ERR_ARG;
+  if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
+  if (N > (1LL << 40)) return BSA_ERR_UNSUPPORTED;
+  return BSA_OK;
+}
+
+// rope may be null: nothing is turned
+int rope_dev(const bsa_rope* rope, long long N, int d, bool inverse, RopeDev* r) {
+  std::memset(r, 0, sizeof(*r));
+  r->sign = inverse ? -1.f : 1.f;
+  r->gh = r->gw = 1;
+  if (!rope) return BSA_OK;
+  if (rope->pairing != BSA_ROPE_ADJACENT && rope->pairing != BSA_ROPE_SPLIT) return BSA_ERR_ARG;
+  long long sum = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (rope->pairs[a] < 0) return BSA_ERR_ARG;
+    sum += rope->pairs[a];
+    if (rope->pairs[a] == 0) continue;
+    if (rope->len[a] < 1 || !rope->table[a] || !aligned(rope->table[a], 8)) return BSA_ERR_ARG;
+    r->table[a] = rope->table[a];
+    r->pairs[a] = rope->pairs[a];
+    r->len[a] = rope->len[a];
+  }
+  if (sum < 1 || sum > d / 2) return BSA_ERR_SHAPE;
+  if (rope->pos) {
+    if (!aligned(rope->pos, 4)) return BSA_ERR_ARG;
+    r->pos = rope->pos;
+    return BSA_OK;
+  }
+  long long n = 1;
+  for (int a = 0; a < 3; ++a) {
+    if (rope->grid[a] < 1 || rope->first[a] < 0) return BSA_ERR_ARG;
+    n *= rope->grid[a];
+    if (n > N || n >= (1LL << 31)) return BSA_ERR_SHAPE;
+    if (rope->pairs[a] > 0 && static_cast<long long>(rope->first[a]) + rope->grid[a] > rope->len[a])
+      return BSA_ERR_SHAPE;
+    r->first[a] = rope->first[a];
+  }
+  r->gh = rope->grid[1];
+  r->gw = rope->grid[2];
+  r->ngrid = n;
+  return BSA_OK;
+}
+
+void set_tensor(RopeTensor* t, const bsa_heads* x, const bsa_heads* g, const bsa_heads* y, const void* w) {
+  t->x = x ? x->data : nullptr;
+  t->xt = x ? x->token_stride : 0;
+  t->xh = x ? x->head_stride : 0;
+  t->g = g ? g->data : nullptr;
+  t->gt = g ? g->token_stride : 0;
+  t->gh = g ? g->head_stride : 0;
+  t->y = y->data;
+  t->yt = y->token_stride;
+  t->yh = y->head_stride;
+  t->H = y->H;
+  t->chunks = (y->H + kRopeHeads - 1) / kRopeHeads;
+  t->per = (y->H + t->chunks - 1) / t->chunks;
+  t->chunks = (y->H + t->per - 1) / t->per;
+  t->w = w;
+}
+
+// blocks that hold every group of the larger tensor, at most `most`
+unsigned rope_blocks(const RopeParams& p, int tensors, int d, long long most) {
+  const int groups = kRopeThreads / (d / 8);
+  long long b = 1;
+  for (int i = 0; i < tensors; ++i) b = std::max(b, (p.N * p.t[i].chunks + groups - 1) / groups);
+  return static_cast<unsigned>(std::min(b, most));
+}
+
+template <typename T, int D>
+int launch_rope_fwd(const RopeParams& p, int tensors, bool split, bool norm, cudaStream_t st) {
+  const dim3 grid(rope_blocks(p, tensors, D, 1LL << 30), tensors);
+  if (split) {
+    if (norm) rope_fwd_kernel<T, D, true, true><<<grid, kRopeThreads, 0, st>>>(p);
+    else rope_fwd_kernel<T, D, true, false><<<grid, kRopeThreads, 0, st>>>(p);
+  } else {
+    if (norm) rope_fwd_kernel<T, D, false, true><<<grid, kRopeThreads, 0, st>>>(p);
+    else rope_fwd_kernel<T, D, false, false><<<grid, kRopeThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int launch_rope_fwd_any(const RopeParams& p, int dtype, int d, int tensors, bool split, bool norm, cudaStream_t st) {
+  if (d == 128) {
+    if (dtype == BSA_BF16) return launch_rope_fwd<__nv_bfloat16, 128>(p, tensors, split, norm, st);
+    if (dtype == BSA_F16) return launch_rope_fwd<__half, 128>(p, tensors, split, norm, st);
+    return launch_rope_fwd<float, 128>(p, tensors, split, norm, st);
+  }
+  if (dtype == BSA_BF16) return launch_rope_fwd<__nv_bfloat16, 64>(p, tensors, split, norm, st);
+  if (dtype == BSA_F16) return launch_rope_fwd<__half, 64>(p, tensors, split, norm, st);
+  return launch_rope_fwd<float, 64>(p, tensors, split, norm, st);
+}
+
+// most blocks of the backward pass: their weight-gradient partial sums are
+// added by one block per tensor afterwards
+constexpr long long kRopeBwdBlocks = 148 * 4;
+
+template <typename T, int D>
+int launch_rope_bwd(const RopeParams& p, int tensors, bool split, unsigned blocks, cudaStream_t st) {
+  const dim3 grid(blocks, tensors);
+  if (split) rope_bwd_kernel<T, D, true><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_bwd_kernel<T, D, false><<<grid, kRopeThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int launch_rope_bwd_any(const RopeParams& p, int dtype, int d, int tensors, bool split, unsigned blocks,
+                        cudaStream_t st) {
+  if (d == 128) {
+    if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 128>(p, tensors, split, blocks, st);
+    if (dtype == BSA_F16) return launch_rope_bwd<__half, 128>(p, tensors, split, blocks, st);
+    return launch_rope_bwd<float, 128>(p, tensors, split, blocks, st);
+  }
+  if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 64>(p, tensors, split, blocks, st);
+  if (dtype == BSA_F16) return launch_rope_bwd<__half, 64>(p, tensors, split, blocks, st);
+  return launch_rope_bwd<float, 64>(p, tensors, split, blocks, st);
+}
+
+// weight type and pointers of the norm
+int check_weights(const void* wq, const void* wk, int dtype, int wtype, float eps) {
+  if (wtype != BSA_F32 && wtype != dtype) return BSA_ERR_ARG;
+  if ((wq && !aligned(wq, 16)) || (wk && !aligned(wk, 16))) return BSA_ERR_ARG;
+  if (!std::isfinite(eps) || !(eps > 0.f)) return BSA_ERR_ARG;
+  return BSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rope_build_table(int len, int pairs, double theta, double start, double step, float* table, void* stream) {
+  if (len < 1 || pairs < 1 || !table || !aligned(table, 8)) return BSA_ERR_ARG;
+  if (!std::isfinite(theta) || !(theta > 0.0) || !std::isfinite(start) || !std::isfinite(step)) return BSA_ERR_ARG;
+  const long long n = static_cast<long long>(len) * pairs;
+  if (n > (1LL << 37)) return BSA_ERR_UNSUPPORTED;
+  rope_table_kernel<<<static_cast<unsigned>((n + 127) / 128), 128, 0, static_cast<cudaStream_t>(stream)>>>(
+      len, pairs, theta, start, step, table);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+int rope_apply(const bsa_heads* x, const bsa_heads* y, int dtype, long long N, int d, const bsa_rope* rope,
+               int inverse, void* stream) {
+  int rc = check_sizes(dtype, N, d);
+  if (rc != BSA_OK) return rc;
+  if (!rope) return BSA_ERR_ARG;
+  if ((rc = check_heads(x, dtype, N, d, false)) != BSA_OK) return rc;
+  if ((rc = check_heads(y, dtype, N, d, true)) != BSA_OK) return rc;
+  if (x->H != y->H) return BSA_ERR_SHAPE;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = N;
+  if ((rc = rope_dev(rope, N, d, inverse != 0, &p.r)) != BSA_OK) return rc;
+  set_tensor(&p.t[0], x, nullptr, y, nullptr);
+  return launch_rope_fwd_any(p, dtype, d, 1, rope->pairing == BSA_ROPE_SPLIT, false,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int qk_norm_rope_fwd(const bsa_heads* q, const bsa_heads* k, const bsa_heads* qo, const bsa_heads* ko, int dtype,
+                     long long N, int d, const void* wq, const void* wk, int wtype, float eps, const bsa_rope* rope,
+                     void* stream) {
+  int rc = check_sizes(dtype, N, d);
+  if (rc != BSA_OK) return rc;
+  if ((rc = check_weights(wq, wk, dtype, wtype, eps)) != BSA_OK) return rc;
+  if ((k == nullptr) != (ko == nullptr)) return BSA_ERR_ARG;
+  const int tensors = k ? 2 : 1;
+  for (int i = 0; i < tensors; ++i) {
+    const bsa_heads* x = i ? k : q;
+    const bsa_heads* y = i ? ko : qo;
+    if ((rc = check_heads(x, dtype, N, d, false)) != BSA_OK) return rc;
+    if ((rc = check_heads(y, dtype, N, d, true)) != BSA_OK) return rc;
+    if (x->H != y->H) return BSA_ERR_SHAPE;
+  }
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = N;
+  p.eps = eps;
+  p.w_f32 = wtype == BSA_F32;
+  if ((rc = rope_dev(rope, N, d, false, &p.r)) != BSA_OK) return rc;
+  set_tensor(&p.t[0], q, nullptr, qo, wq);
+  if (k) set_tensor(&p.t[1], k, nullptr, ko, wk);
+  return launch_rope_fwd_any(p, dtype, d, tensors, rope && rope->pairing == BSA_ROPE_SPLIT, true,
+                             static_cast<cudaStream_t>(stream));
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(long long N, int Hq, int Hk, int d) {
+  if (N < 1 || Hq < 1 || Hk < 0 || (d != 64 && d != 128)) return static_cast<size_t>(-1);
+  return static_cast<size_t>(2) * kRopeBwdBlocks * d * sizeof(float);
+}
+
+int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* q, const bsa_heads* k,
+                     const bsa_heads* dq, const bsa_heads* dk, int dtype, long long N, int d, const void* wq,
+                     const void* wk, int wtype, float eps, const bsa_rope* rope, float* dwq, float* dwk,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_sizes(dtype, N, d);
+  if (rc != BSA_OK) return rc;
+  if ((rc = check_weights(wq, wk, dtype, wtype, eps)) != BSA_OK) return rc;
+  if ((k == nullptr) != (gk == nullptr) || (k == nullptr) != (dk == nullptr)) return BSA_ERR_ARG;
+  if (!k && dwk) return BSA_ERR_ARG;
+  if ((dwq && !aligned(dwq, 4)) || (dwk && !aligned(dwk, 4))) return BSA_ERR_ARG;
+  const int tensors = k ? 2 : 1;
+  for (int i = 0; i < tensors; ++i) {
+    const bsa_heads* x = i ? k : q;
+    const bsa_heads* g = i ? gk : gq;
+    const bsa_heads* y = i ? dk : dq;
+    if ((rc = check_heads(x, dtype, N, d, false)) != BSA_OK) return rc;
+    if ((rc = check_heads(g, dtype, N, d, false)) != BSA_OK) return rc;
+    if ((rc = check_heads(y, dtype, N, d, true)) != BSA_OK) return rc;
+    if (x->H != y->H || g->H != y->H) return BSA_ERR_SHAPE;
+  }
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = N;
+  p.eps = eps;
+  p.w_f32 = wtype == BSA_F32;
+  if ((rc = rope_dev(rope, N, d, true, &p.r)) != BSA_OK) return rc;
+  if (!workspace || !aligned(workspace, 256) ||
+      ws_bytes < qk_norm_rope_bwd_workspace_bytes(N, q->H, k ? k->H : 0, d))
+    return BSA_ERR_WORKSPACE;
+  set_tensor(&p.t[0], q, gq, dq, wq);
+  if (k) set_tensor(&p.t[1], k, gk, dk, wk);
+  p.partial = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned blocks = rope_blocks(p, tensors, d, kRopeBwdBlocks);
+  rc = launch_rope_bwd_any(p, dtype, d, tensors, rope && rope->pairing == BSA_ROPE_SPLIT, blocks, st);
+  if (rc != BSA_OK || (!dwq && !dwk)) return rc;
+  rope_dw_kernel<<<tensors, 1024, 0, st>>>(p.partial, static_cast<int>(blocks), d, dwq, dwk);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // extern "C"

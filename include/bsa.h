@@ -297,6 +297,131 @@ int blocksparse_attn_fwd_noalloc(const void* q, const void* k, const void* v,
                                  const bsa_index* index, void* o, float* lse,
                                  void* stream);
 
+/* Element types of bsa_heads tensors and norm weights. */
+enum {
+  BSA_BF16 = 0,
+  BSA_F16 = 1,
+  BSA_F32 = 2
+};
+
+/* Which two channels of a row of d form pair j (0 <= j < d/2). */
+enum {
+  BSA_ROPE_ADJACENT = 0,   /* channels 2j and 2j + 1                        */
+  BSA_ROPE_SPLIT = 1       /* channels j and j + d/2                        */
+};
+
+/*
+ * One [N, H, d] tensor given by strides (host struct; `data` is device
+ * memory): element (n, h, c) is data[n * token_stride + h * head_stride + c],
+ * strides in elements, so that q and k may be slices of one packed
+ * projection.  data and both strides (in bytes) are multiples of 16.
+ * Offsets are computed in 64 bits: N * token_stride may pass 2^31.
+ * Strides of inputs are >= 0 (0 repeats the same row); the rows of an output
+ * must not overlap one another: the smaller of the two strides is at least d
+ * and the larger at least the smaller times its extent (H or N).
+ */
+typedef struct bsa_heads {
+  void* data;
+  int H;
+  long long token_stride, head_stride;
+} bsa_heads;
+
+/*
+ * Rotary positions over up to three axes (time, height, width); host struct,
+ * the tables and pos are device memory.
+ *   pairing: BSA_ROPE_ADJACENT or BSA_ROPE_SPLIT.
+ *   pairs[a]: channel pairs turned by axis a, dealt in order (pairs 0 ..
+ *     pairs[0]-1 by axis 0, and so on); >= 0 each, their sum in [1, d/2].
+ *     Pairs behind the last axis are copied unturned.
+ *   table[a]: float32 [len[a]][pairs[a]][2], (cos, sin) per position and pair
+ *     of axis a (rope_build_table fills one); 8-byte aligned; ignored where
+ *     pairs[a] is 0.
+ *   pos == NULL: token n < grid[0] * grid[1] * grid[2] (row-major; at most N
+ *     and below 2^31) sits at first[a] + its grid coordinate, which must be
+ *     inside every table (checked on the host); tokens behind the grid (text
+ *     or padding) are not turned.
+ *   pos != NULL: int32 [N][3]; a negative position is not turned along its
+ *     axis, one >= len[a] is not turned either and is reported as
+ *     BSA_ERR_INDEX_RANGE through the device status word.  grid and first are
+ *     ignored.
+ */
+typedef struct bsa_rope {
+  int pairing;
+  int pairs[3];
+  int len[3];
+  const float* table[3];
+  int grid[3];
+  int first[3];
+  const int32_t* pos;
+} bsa_rope;
+
+/*
+ * rope_build_table - cos and sin of the angles of one axis.
+ *
+ * table[i][j] = (cos a, sin a), a = (start + i * step) * theta^(-j / pairs):
+ * the angle and both functions in 64 bits, rounded once to float32.
+ * (step scales the positions of a video longer than the trained horizon.)
+ * table: out, device float32 [len][pairs][2], 8-byte aligned.
+ * Limits: len >= 1, pairs >= 1, theta > 0, theta, start and step finite.
+ * Returns BSA_OK, or BSA_ERR_ARG / BSA_ERR_CUDA.
+ */
+int rope_build_table(int len, int pairs, double theta, double start, double step,
+                     float* table, void* stream);
+
+/*
+ * rope_apply - turn queries or keys by their positions.
+ *
+ * For every token n, head h and pair j with the angle a of its position:
+ *   (y_a, y_b) = (x_a cos a - x_b sin a, x_a sin a + x_b cos a)
+ * in float32, rounded once.  inverse != 0 turns by -a, which undoes the call
+ * and is its gradient.
+ *
+ * x: in; y: out, same H; y may be x itself (same data and strides), otherwise
+ * the two must not overlap.  dtype: BSA_BF16, BSA_F16 or BSA_F32, of both.
+ * Returns BSA_OK or a negative bsa_status.
+ */
+int rope_apply(const bsa_heads* x, const bsa_heads* y, int dtype, long long N, int d,
+               const bsa_rope* rope, int inverse, void* stream);
+
+/*
+ * qk_norm_rope_fwd - per-head RMS norm of queries and keys and their
+ * rotation, in one pass over the data.
+ *
+ *   z = x * (mean_c x_c^2 + eps)^(-1/2) * w,  y = z turned as by rope_apply
+ * over the d channels of every (token, head), in float32, rounded once.
+ *
+ * q, k: in; qo, ko: out, same H as q and k (H of q and k may differ); an
+ * output may be its own input, otherwise nothing may overlap.  k and ko may
+ * both be NULL (queries alone).  wq, wk: device [d], 16-byte aligned, of type
+ * wtype (BSA_F32 or the tensors' dtype), or NULL for a norm without weights.
+ * eps: finite, > 0.  rope: NULL for the norm alone.
+ * Returns BSA_OK or a negative bsa_status.
+ */
+int qk_norm_rope_fwd(const bsa_heads* q, const bsa_heads* k, const bsa_heads* qo, const bsa_heads* ko, int dtype,
+                     long long N, int d, const void* wq, const void* wk, int wtype, float eps,
+                     const bsa_rope* rope, void* stream);
+
+/*
+ * qk_norm_rope_bwd - gradient of qk_norm_rope_fwd.
+ *
+ * gq, gk: in, gradients of qo and ko; q, k, wq, wk, eps, rope: as given to
+ * the forward call.  dq, dk: out, gradients of q and k (dtype; each may be
+ * its gq / gk or its q / k).  dwq, dwk: out, device float32 [d], gradients of
+ * the weights, summed over tokens and heads in a fixed order (the same from
+ * run to run); NULL where they are not wanted.  gk, k and dk may be NULL
+ * together (then dwk must be NULL).
+ * workspace: device, 256-byte aligned, at least
+ * qk_norm_rope_bwd_workspace_bytes(N, H of q, H of k or 0, d) bytes;
+ * overwritten.
+ * Returns BSA_OK or a negative bsa_status.
+ */
+int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* q, const bsa_heads* k,
+                     const bsa_heads* dq, const bsa_heads* dk, int dtype, long long N, int d,
+                     const void* wq, const void* wk, int wtype, float eps, const bsa_rope* rope,
+                     float* dwq, float* dwk, void* workspace, size_t ws_bytes, void* stream);
+/* Scratch bytes of qk_norm_rope_bwd; (size_t)-1 for invalid arguments. */
+size_t qk_norm_rope_bwd_workspace_bytes(long long N, int Hq, int Hk, int d);
+
 /* Operation codes for bsa_workspace_bytes. */
 enum {
   BSA_OP_BLOCKSPARSE_FWD = 1,

@@ -45,7 +45,7 @@ EXPORTED = ("lvsa_build_index", "lvsa_build_index_window", "attn_dense_blockmass
             "bsa_workspace_bytes", "bsa_get_device_status", "bsa_status_string",
             "bsa_debug_expired_wait", "bsa_version", "blocksparse_attn_fwd_noalloc",
             "rope_build_table", "rope_apply", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
-            "qk_norm_rope_bwd_workspace_bytes")
+            "qk_norm_rope_bwd_workspace_bytes", "blockmean_select", "blockmean_select_workspace_bytes")
 
 
 class BsaError(RuntimeError):
@@ -119,6 +119,8 @@ def _load():
         "qk_norm_rope_fwd": (I, [HP, HP, HP, HP, I, L, I, P, P, I, F, RP, P]),
         "qk_norm_rope_bwd": (I, [HP, HP, HP, HP, HP, HP, I, L, I, P, P, I, F, RP, P, P, P, SZ, P]),
         "qk_norm_rope_bwd_workspace_bytes": (SZ, [L, I, I, I]),
+        "blockmean_select": (I, [P, P, I, I, I, I, I, I, P, P, P, SZ, P]),
+        "blockmean_select_workspace_bytes": (SZ, [I, I, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -626,6 +628,36 @@ def qk_norm_rope_bwd(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tens
                                    workspace.numel() * workspace.element_size(), st)
     _check("qk_norm_rope_bwd", rc)
     return dq, dk, dwq, dwk
+
+
+# ------------------------------------------------ key blocks by block means ---
+def blockmean_select(q: torch.Tensor, k: torch.Tensor, keep: int, local: int = 0, block: int = 128, idx=None, cnt=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Per (head, query block) the ``keep`` key blocks of the largest mean score, the blocks
+    within ``local`` of the own one always among them (-1: none forced); returns
+    (idx [H,nB,nB] int32 ascending, -1 padded, cnt [H,nB] int32) for block_index."""
+    _check_qkv(q, k, k)
+    if k.device != q.device:
+        raise ValueError(f"k must be on {q.device}, got {k.device}")
+    _check_workspace(workspace, q.device)
+    N, H, d = q.shape
+    nB = math.ceil(N / 128)
+    _check_tensor("idx", idx, (H, nB, nB), torch.int32, q.device)
+    _check_tensor("cnt", cnt, (H, nB), torch.int32, q.device)
+    need = int(_lib.blockmean_select_workspace_bytes(N, H, d))
+    if need == ctypes.c_size_t(-1).value:
+        raise BsaError("blockmean_select", BSA_ERR_UNSUPPORTED)
+    with _on_device(q.device, stream) as st:
+        if idx is None:
+            idx = torch.empty((H, nB, nB), dtype=torch.int32, device=q.device)
+        if cnt is None:
+            cnt = torch.empty((H, nB), dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        rc = _lib.blockmean_select(_ptr(q), _ptr(k), N, H, d, int(block), int(keep), int(local), _ptr(idx), _ptr(cnt),
+                                   _ptr(workspace), workspace.numel() * workspace.element_size(), st)
+    _check("blockmean_select", rc, (BSA_OK, BSA_WARN_OVER_BUDGET))
+    return idx, cnt
 
 
 def get_device_status(stream=None) -> int:

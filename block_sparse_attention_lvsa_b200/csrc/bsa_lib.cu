@@ -18,6 +18,7 @@
 #include "attn_fwd.cuh"
 #include "blockmass.cuh"
 #include "rope.cuh"
+#include "blockmean.cuh"
 
 namespace {
 
@@ -708,6 +709,74 @@ int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* 
   if (rc != BSA_OK || (!dwq && !dwk)) return rc;
   rope_dw_kernel<<<tensors, 1024, 0, st>>>(p.partial, static_cast<int>(blocks), d, dwq, dwk);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Key blocks by block means.
+namespace {
+
+// per-device opt-in to large dynamic shared memory, set once per kernel
+template <typename K>
+int allow_smem(K* kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BSA_ERR_CUDA;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return BSA_ERR_CUDA;
+    done[dev].store(true, std::memory_order_release);
+  }
+  return BSA_OK;
+}
+
+constexpr int kMeanSelectSmem = 96 * 1024;            // keys of all warps of a block
+
+template <int D>
+int launch_mean_select(const double* mean, int H, int nB, int keep, int local, int32_t* idx, int32_t* cnt,
+                       cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  int rc = allow_smem(blockmean_select_kernel<D>, kMeanSelectSmem, done);
+  if (rc != BSA_OK) return rc;
+  const int wpc = std::min(8, std::max(1, kMeanSelectSmem / (nB * 8)));
+  const dim3 grid((nB + wpc - 1) / wpc, H);
+  blockmean_select_kernel<D><<<grid, wpc * 32, static_cast<size_t>(wpc) * nB * 8, st>>>(mean, H, nB, keep, local, idx,
+                                                                                     cnt);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t blockmean_select_workspace_bytes(int N, int H, int d) {
+  if (N < 1 || H < 1 || H > 65535 || (d != 64 && d != 128) || n_tiles(N) > kMeanMaxBlocks)
+    return static_cast<size_t>(-1);
+  return round_up(static_cast<size_t>(2) * H * n_tiles(N) * d * sizeof(double), 256);
+}
+
+int blockmean_select(const void* q, const void* k, int N, int H, int d, int block, int keep, int local, int32_t* idx,
+                     int32_t* cnt, void* workspace, size_t ws_bytes, void* stream) {
+  if (!q || !k || !idx || !cnt || !aligned(q, 16) || !aligned(k, 16) || !aligned(idx, 4) || !aligned(cnt, 4))
+    return BSA_ERR_ARG;
+  if (N < 1 || H < 1 || H > 65535 || keep < 1 || local < -1) return BSA_ERR_ARG;
+  if (block != 128 || (d != 64 && d != 128)) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * H * d >= (1LL << 31) || n_tiles(N) > kMeanMaxBlocks) return BSA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < blockmean_select_workspace_bytes(N, H, d))
+    return BSA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int nB = n_tiles(N);
+  local = std::min(local, nB);
+  double* mean = static_cast<double*>(workspace);
+  const dim3 grid(nB, (H * d + 255) / 256, 2);
+  blockmean_pool_kernel<<<grid, kPoolThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(q),
+                                                       static_cast<const __nv_bfloat16*>(k), N, H, d, nB, mean);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  const int rc = d == 128 ? launch_mean_select<128>(mean, H, nB, keep, local, idx, cnt, st)
+                          : launch_mean_select<64>(mean, H, nB, keep, local, idx, cnt, st);
+  if (rc != BSA_OK) return rc;
+  // the widest neighbourhood of any row
+  return std::min<long long>(nB, 2LL * local + 1) > keep ? BSA_WARN_OVER_BUDGET : BSA_OK;
 }
 
 }  // extern "C"

@@ -297,6 +297,34 @@ int blocksparse_attn_fwd_noalloc(const void* q, const void* k, const void* v,
                                  const bsa_index* index, void* o, float* lse,
                                  void* stream);
 
+/*
+ * blockmean_select - per (head, query block) the key blocks of the largest
+ * mean score, for the block-sparse attention.
+ *
+ * For 128-token blocks i of q and j of k (the last one may be short), per head
+ *   s(i, j) = < mean of q over block i, mean of k over block j >,
+ * the mean of the tile's scores <q, k>.  Row i keeps its neighbourhood
+ * |i - j| <= local and then the blocks of the largest s, at equal scores the
+ * lower j first, until it holds max(min(keep, nB), size of the neighbourhood)
+ * blocks; the list is written ascending.  Means and deciding scores are
+ * computed in 64 bits; a score that is not a number counts as the lowest.
+ * Unlike losa_select this needs no dense step: q and k are read once.
+ *
+ * q, k: in, bf16 [N,H,d].  block: must be 128.  keep >= 1.  local >= -1 (-1:
+ * no neighbourhood, 0: the own block).
+ * idx: out, int32 [H][nB][nB], kept ids ascending, then -1 padding; cnt: out,
+ * int32 [H][nB] (an index of kind BSA_INDEX_BLOCKS).
+ * workspace: device, 256-byte aligned, at least
+ * blockmean_select_workspace_bytes(N, H, d) bytes; overwritten.
+ * Limits: ceil(N / 128) <= 8192.
+ * Returns BSA_OK, BSA_WARN_OVER_BUDGET (some neighbourhood holds more than
+ * `keep` blocks) or a negative bsa_status.
+ */
+int blockmean_select(const void* q, const void* k, int N, int H, int d, int block, int keep, int local,
+                     int32_t* idx, int32_t* cnt, void* workspace, size_t ws_bytes, void* stream);
+/* Scratch bytes of blockmean_select; (size_t)-1 for invalid arguments. */
+size_t blockmean_select_workspace_bytes(int N, int H, int d);
+
 /* Element types of bsa_heads tensors and norm weights. */
 enum {
   BSA_BF16 = 0,

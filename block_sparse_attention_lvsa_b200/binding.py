@@ -34,6 +34,7 @@ BSA_INDEX_LVSA_BLOCKS = 3
 BSA_OP_BLOCKSPARSE_FWD = 1
 BSA_OP_DENSE_BLOCKMASS = 2
 BSA_OP_BLOCKMASS = 3
+BSA_OP_BLOCKSPARSE_BWD = 4
 
 BSA_BF16 = 0
 BSA_F16 = 1
@@ -45,7 +46,8 @@ EXPORTED = ("lvsa_build_index", "lvsa_build_index_window", "attn_dense_blockmass
             "bsa_workspace_bytes", "bsa_get_device_status", "bsa_status_string",
             "bsa_debug_expired_wait", "bsa_version", "blocksparse_attn_fwd_noalloc",
             "rope_build_table", "rope_apply", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
-            "qk_norm_rope_bwd_workspace_bytes", "blockmean_select", "blockmean_select_workspace_bytes")
+            "qk_norm_rope_bwd_workspace_bytes", "blockmean_select", "blockmean_select_workspace_bytes",
+            "blocksparse_attn_bwd")
 
 
 class BsaError(RuntimeError):
@@ -121,6 +123,7 @@ def _load():
         "qk_norm_rope_bwd_workspace_bytes": (SZ, [L, I, I, I]),
         "blockmean_select": (I, [P, P, I, I, I, I, I, I, P, P, P, SZ, P]),
         "blockmean_select_workspace_bytes": (SZ, [I, I, I]),
+        "blocksparse_attn_bwd": (I, [P, P, P, P, HP, P, I, I, I, F, ctypes.POINTER(bsa_index), P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -658,6 +661,42 @@ def blockmean_select(q: torch.Tensor, k: torch.Tensor, keep: int, local: int = 0
                                    _ptr(workspace), workspace.numel() * workspace.element_size(), st)
     _check("blockmean_select", rc, (BSA_OK, BSA_WARN_OVER_BUDGET))
     return idx, cnt
+
+
+# ------------------------------------------------- gradient of the attention ---
+def blocksparse_attn_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                         lse: torch.Tensor, index: bsa_index, scale: Optional[float] = None,
+                         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                         dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of blocksparse_attn_fwd: (dq, dk, dv), each bf16 [N,H,d], for the gradient go of o.
+    o and lse are the forward call's results for the same q, k, v, index and scale (o may be
+    a strided copy)."""
+    _check_qkv(q, k, v)
+    N, H, d = q.shape
+    dev = q.device
+    for name, t in (("k", k), ("v", v), ("go", go), ("dq", dq), ("dk", dk), ("dv", dv)):
+        _check_tensor(name, t, q.shape, torch.bfloat16, dev)
+    for name, t in (("go", go), ("o", o), ("lse", lse)):
+        if t is None:
+            raise ValueError(f"{name} must be given")
+    ho = _heads("o", o, q)
+    _check_tensor("lse", lse, (H, N), torch.float32, dev)
+    _check_workspace(workspace, dev)
+    for t in getattr(index, "_tensors", ()):
+        if t.device != dev:
+            raise ValueError(f"the index is on {t.device}, the tensors on {dev}")
+    if scale is None:
+        scale = d ** -0.5
+    need = workspace_bytes(BSA_OP_BLOCKSPARSE_BWD, N, H, d, index)
+    with _on_device(dev, stream) as st:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        dq, dk, dv = (torch.empty_like(q) if t is None else t for t in (dq, dk, dv))
+        rc = _lib.blocksparse_attn_bwd(_ptr(go), _ptr(q), _ptr(k), _ptr(v), ctypes.byref(ho), _ptr(lse), N, H, d, float(scale),
+                                       ctypes.byref(index), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), st)
+    _check("blocksparse_attn_bwd", rc)
+    return dq, dk, dv
 
 
 def get_device_status(stream=None) -> int:

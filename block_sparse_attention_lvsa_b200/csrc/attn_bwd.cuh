@@ -1,0 +1,725 @@
+// attn_bwd.cuh - gradient of the block-sparse softmax attention on sm_100a
+// tensor cores (tcgen05 + TMEM + TMA).
+//
+// With s = scale <q, k>, p = exp(s - lse) the forward's probabilities and
+// D_q = <do_q, o_q> = sum_k p <do_q, v_k>:
+//   dv_k = sum_q p do_q
+//   ds   = p (<do_q, v_k> - D_q)
+//   dq_q = scale sum_k ds k_k,     dk_k = scale sum_q ds q_q
+// over the pairs that the index admits.  lse comes from the forward, so a
+// tile needs no running maximum and tiles can be taken in any grouping.
+//
+// Two kernels, each with every sum of its outputs inside one CTA (no atomics:
+// the result does not change from run to run), at the price of forming s and
+// <do, v> twice (7 products of 128 x 128 x d a tile instead of 5):
+//   attn_bwd_dkv_kernel  one CTA per 128-key tile and head, over the query
+//     tiles that list it (the index transposed on the device).  Tiles are
+//     held transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and dS^T
+//     (bf16, written over them in TMEM) are the A operands of
+//     dV += P^T dO and dK += dS^T Q and never touch shared memory.
+//   attn_bwd_dq_kernel   one CTA per 128-query tile and head, over its own
+//     list: S = Q K^T, dP = dO V^T, dQ += dS K.
+//
+// Warp roles (384 threads), as in the forward:
+//   warp 0        TMA producer          warp 1   tcgen05.mma issuer
+//   warps 4..7    columns 0..63 of every tile (thread = TMEM lane = row)
+//   warps 8..11   columns 64..127
+// A thread turns 64 scores into probabilities (kept in registers in 32 bits
+// for ds) while the tensor core runs the products of the neighbouring steps:
+//   dkv:  dV(i), S(i+1) | dK(i), dP(i+1)       dq:  dP(j+1), dQ(j), S(j+2)
+// P and dS are rounded to bf16 for the products (half a step, at most 2^-8
+// of each term, as P is in the forward); all sums are 32-bit.  Each half of the
+// columns is written over its own half of the scores, so the two warpgroups
+// never wait for one another.
+#pragma once
+#include "attn_fwd.cuh"
+
+namespace bsa {
+
+struct BwdParams {
+  int N, H, nB;
+  float sl2;                        // scale * log2(e)
+  float scale;
+  // dq: key-tile lists of the query tiles (see AttnParams)
+  const int32_t* list;
+  const int32_t* count;
+  const uint8_t* flags;
+  long long lhs;
+  int lrs, chs;
+  // dkv: query-tile lists of the key tiles, entry = tile | partial << 30
+  const int32_t* tlist;
+  const int32_t* tcount;
+  long long tlhs;                   // head stride (0: shared by all heads)
+  int tchs;
+  // element mask (LVSA)
+  const uint32_t* fbits;
+  int TW, P;
+  // per (head, token), padded to nB * 128: -lse * log2(e) (-inf: no key) and -D
+  const float* nl;
+  const float* nd;
+  long long wait_limit_ns;
+};
+
+constexpr int kBwdThreads = 384;
+constexpr int kPartialBit = 1 << 30;
+
+// 64 consecutive columns of the thread's TMEM lane, complete on return
+__device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+               : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// untiled copy global -> shared (16-byte aligned addresses and size), completes on `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// nl = -lse * log2(e) and nd = -<do, o> per (head, token), [H][nB * 128];
+// tokens past N and rows without a key get nl = -inf (p = 0).  d/8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const __nv_bfloat16* __restrict__ o,
+                                                            long long o_ts, long long o_hs,
+                                                            const __nv_bfloat16* __restrict__ go,
+                                                            const float* __restrict__ lse, int N, int H, int NP,
+                                                            float* __restrict__ nl, float* __restrict__ nd) {
+  constexpr int G = D / 8;
+  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;   // n * H + h
+  const int l = threadIdx.x % G;
+  const long long n = row / H;
+  const int h = static_cast<int>(row - n * H);
+  float sum = 0.f;
+  if (n < N) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+      sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
+    }
+  }
+#pragma unroll
+  for (int s = G / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+  if (l == 0 && n < NP) {
+    const size_t at = static_cast<size_t>(h) * NP + n;
+    const float e = n < N ? lse[static_cast<size_t>(h) * N + n] : -INFINITY;
+    nl[at] = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
+    nd[at] = -sum;
+  }
+}
+
+// Bit sets of the rows' lists: bits[h][w][qb] bit b = key tile 32 w + b is
+// listed by query tile qb, and the same of the partial ones.  One warp per
+// row; 8192 tiles at a time in shared memory.  Entries out of range are
+// skipped and, like repeated ones, reported.
+__global__ void __launch_bounds__(128) attn_bwd_bits_kernel(const int32_t* __restrict__ list,
+                                                            const int32_t* __restrict__ count,
+                                                            const uint8_t* __restrict__ flags, long long lhs, int lrs,
+                                                            int chs, int nB, uint32_t* __restrict__ bits,
+                                                            uint32_t* __restrict__ part) {
+  constexpr int kWords = 256;
+  __shared__ uint32_t s_on[4][kWords], s_part[4][kWords];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qb = blockIdx.x * 4 + warp, h = blockIdx.y;
+  if (qb >= nB) return;
+  const int nW = (nB + 31) / 32;
+  int n = count[static_cast<size_t>(h) * chs + qb];
+  bool bad = n < 0 || n > lrs;
+  n = min(max(n, 0), lrs);
+  const size_t off = static_cast<size_t>(h) * lhs + static_cast<size_t>(qb) * lrs;
+  for (int w0 = 0; w0 < nW; w0 += kWords) {
+    const int words = min(kWords, nW - w0);
+    for (int w = lane; w < words; w += 32) s_on[warp][w] = s_part[warp][w] = 0u;
+    __syncwarp();
+    for (int j = lane; j < n; j += 32) {
+      const int kt = list[off + j];
+      if (kt < 0 || kt >= nB) {
+        bad = true;
+        continue;
+      }
+      const int w = (kt >> 5) - w0;
+      if (w < 0 || w >= words) continue;
+      const uint32_t b = 1u << (kt & 31);
+      if (atomicOr(&s_on[warp][w], b) & b) bad = true;
+      if (flags != nullptr && flags[off + j]) atomicOr(&s_part[warp][w], b);
+    }
+    __syncwarp();
+    for (int w = lane; w < words; w += 32) {
+      const size_t at = (static_cast<size_t>(h) * nW + w0 + w) * nB + qb;
+      bits[at] = s_on[warp][w];
+      if (part != nullptr) part[at] = s_part[warp][w];
+    }
+    __syncwarp();
+  }
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(BSA_ERR_INDEX_RANGE);
+}
+
+// Query-tile lists of the key tiles, ascending.  One warp per 32 key tiles of
+// a head: lane = key tile, 32 query tiles' words per load.
+__global__ void __launch_bounds__(128) attn_bwd_lists_kernel(int nB, const uint32_t* __restrict__ bits,
+                                                             const uint32_t* __restrict__ part,
+                                                             int32_t* __restrict__ tlist, int32_t* __restrict__ tcount) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nW = (nB + 31) / 32;
+  const int w = blockIdx.x * 4 + warp, h = blockIdx.y;
+  if (w >= nW) return;
+  const int kt = w * 32 + lane;
+  const uint32_t* on = bits + (static_cast<size_t>(h) * nW + w) * nB;
+  const uint32_t* pt = part == nullptr ? nullptr : part + (static_cast<size_t>(h) * nW + w) * nB;
+  int32_t* out = tlist + (static_cast<size_t>(h) * nB + min(kt, nB - 1)) * nB;   // lanes past nB write nothing: their bits are 0
+  int n = 0;
+  for (int q0 = 0; q0 < nB; q0 += 32) {
+    const uint32_t a = q0 + lane < nB ? on[q0 + lane] : 0u;
+    const uint32_t b = (pt != nullptr && q0 + lane < nB) ? pt[q0 + lane] : 0u;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t x = __shfl_sync(0xFFFFFFFFu, a, i), y = __shfl_sync(0xFFFFFFFFu, b, i);
+      if ((x >> lane) & 1u) out[n++] = (q0 + i) | (((y >> lane) & 1u) ? kPartialBit : 0);
+    }
+  }
+  if (kt < nB) tcount[static_cast<size_t>(h) * nB + kt] = n;
+}
+
+__device__ __forceinline__ void set_bits64(uint32_t (&mw)[2], int a, int b) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int lo = max(a, 32 * w), hi = min(b, 32 * w + 32);
+    if (lo < hi) mw[w] |= (hi - lo == 32 ? 0xFFFFFFFFu : ((1u << (hi - lo)) - 1u)) << (lo - 32 * w);
+  }
+}
+__device__ __forceinline__ bool frame_bit(const BwdParams& p, int fq, int fk) {
+  return (__ldg(p.fbits + static_cast<size_t>(fq) * p.TW + (fk >> 5)) >> (fk & 31)) & 1u;
+}
+// Element mask of 64 query columns for key frame fk: bit c set iff query q0+c
+// < N may attend it.
+__device__ __forceinline__ void query_mask(const BwdParams& p, int fk, int q0, uint32_t (&mw)[2]) {
+  mw[0] = mw[1] = 0u;
+  const int qend = min(q0 + 64, p.N);
+  for (int f = q0 / p.P; f * p.P < qend; ++f)
+    if (frame_bit(p, f, fk)) set_bits64(mw, max(f * p.P, q0) - q0, min((f + 1) * p.P, qend) - q0);
+}
+// Element mask of 64 key columns for query frame fq (no frames: every key < N).
+__device__ __forceinline__ void key_mask(const BwdParams& p, int fq, int k0, uint32_t (&mw)[2]) {
+  mw[0] = mw[1] = 0u;
+  const int kend = min(k0 + 64, p.N);
+  if (p.fbits == nullptr) {
+    set_bits64(mw, 0, kend - k0);
+    return;
+  }
+  for (int f = k0 / p.P; f * p.P < kend; ++f)
+    if (frame_bit(p, fq, f)) set_bits64(mw, max(f * p.P, k0) - k0, min((f + 1) * p.P, kend) - k0);
+}
+
+// One row of an f32 accumulator (TMEM) to bf16 in a 128-byte-swizzled tile in
+// shared memory, times `mul`; zeros when !have.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sTile, int r, float mul, bool have) {
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t ov[32];
+    __syncwarp();
+    if (have) {
+      tmem_ld_x32(tAcc + c0, ov);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) ov[c] = 0u;
+    }
+#pragma unroll
+    for (int v4 = 0; v4 < 4; ++v4) {
+      const int col = c0 + 8 * v4;
+      const uint32_t dst = sTile + (col / 64) * (128 * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) * 16);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(ov[8 * v4 + 2 * i]) * mul, __uint_as_float(ov[8 * v4 + 2 * i + 1]) * mul);
+      st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+template <int D>
+struct BwdSmem {
+  static constexpr uint32_t kBox = 128 * 128;
+  static constexpr uint32_t kTile = (D / 64) * kBox;
+  // dkv: K, V, then two stages of Q, dO, and of nl, nd (128 floats each)
+  // dq:  Q, dO, then three K and two V tiles
+  static constexpr uint32_t kA = 0, kB = kTile, kRing = 2 * kTile;
+  static constexpr uint32_t kBar = kRing + 5 * kTile;
+  static constexpr uint32_t kHolder = kBar + 32 * 8;
+  static constexpr uint32_t kAlloc = kHolder + 16 + 1024;           // + alignment slack
+};
+// dkv keeps nl and nd in the fifth ring tile
+template <int D>
+constexpr uint32_t kDkvRows = BwdSmem<D>::kRing + 4 * BwdSmem<D>::kTile;
+
+enum : int { W_AB = 0, W_QFULL = 1, W_OFULL = 3, W_QEMPTY = 5, W_OEMPTY = 7, W_SFULL = 9, W_DPFULL = 10, W_P = 11, W_DS = 13, W_FINAL = 15 };
+
+// dK and dV of one key tile.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
+                    const BwdParams p) {
+  using L = BwdSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t bar0 = base + L::kBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + L::kHolder);
+
+  const int kt = blockIdx.x, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = p.wait_limit_ns;
+  const int n = p.tcount[static_cast<size_t>(h) * p.tchs + kt];
+  const int32_t* lst = p.tlist + static_cast<size_t>(h) * p.tlhs + static_cast<size_t>(kt) * p.nB;
+  const int NP = p.nB * 128;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 16; ++i) mbar_init(bar(i), (i >= W_P && i < W_FINAL) ? 4 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::kHolder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *holder;
+  constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 256, kTDK = 256 + D;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdescD = idesc_bf16_f32(128, D, false, true);
+  auto sQ = [&](int i) -> uint32_t { return base + L::kRing + (i & 1) * 2 * L::kTile; };
+  auto sG = [&](int i) -> uint32_t { return base + L::kRing + ((i & 1) * 2 + 1) * L::kTile; };
+  auto sRow = [&](int i) -> uint32_t { return base + kDkvRows<D> + (i & 1) * 1024; };
+
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(bar(W_AB), 2 * L::kTile);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        tma_load_3d(base + L::kA + b * L::kBox, &tmK, bar(W_AB), b * 64, h, kt * 128);
+        tma_load_3d(base + L::kB + b * L::kBox, &tmV, bar(W_AB), b * 64, h, kt * 128);
+      }
+      int nq = 0, no = 0;                               // copies started
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        const int qt = lst[i] & ~kPartialBit;
+        if (i >= 2) ok = mbar_wait(bar(W_QEMPTY + (i & 1)), ((i >> 1) - 1) & 1, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(W_QFULL + (i & 1)), L::kTile + 1024);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(sQ(i) + b * L::kBox, &tmQ, bar(W_QFULL + (i & 1)), b * 64, h, qt * 128);
+        const size_t at = static_cast<size_t>(h) * NP + static_cast<size_t>(qt) * 128;
+        bulk_load(sRow(i), p.nl + at, 512, bar(W_QFULL + (i & 1)));
+        bulk_load(sRow(i) + 512, p.nd + at, 512, bar(W_QFULL + (i & 1)));
+        ++nq;
+        if (i >= 2) ok = mbar_wait(bar(W_OEMPTY + (i & 1)), ((i >> 1) - 1) & 1, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(W_OFULL + (i & 1)), L::kTile);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(sG(i) + b * L::kBox, &tmG, bar(W_OFULL + (i & 1)), b * 64, h, qt * 128);
+        ++no;
+      }
+      // drain: wait (bounded) for this thread's own copies still in flight
+      mbar_wait(bar(W_AB), 0, limit);
+      for (int u = max(0, nq - 2); u < nq; ++u) mbar_wait(bar(W_QFULL + (u & 1)), (u >> 1) & 1, limit);
+      for (int u = max(0, no - 2); u < no; ++u) mbar_wait(bar(W_OFULL + (u & 1)), (u >> 1) & 1, limit);
+    }
+  } else if (warp == 1) {
+    if (n > 0) {
+      const uint64_t dK = desc64(sw128_desc(base + L::kA, 16, 1024)), dV = desc64(sw128_desc(base + L::kB, 16, 1024));
+      // S^T = K Q_i^T
+      auto s_mma = [&](int i) {
+        const uint64_t dq = desc64(sw128_desc(sQ(i), 16, 1024));
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+          mma4_ss_warp(tbase + kTS, dK + g * (L::kBox >> 4), dq + g * (L::kBox >> 4), kIdescS, g > 0);
+        tc_commit_warp(bar(W_SFULL));
+      };
+      // dP^T = V dO_i^T
+      auto dp_mma = [&](int i) {
+        const uint64_t dg = desc64(sw128_desc(sG(i), 16, 1024));
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+          mma4_ss_warp(tbase + kTDP, dV + g * (L::kBox >> 4), dg + g * (L::kBox >> 4), kIdescS, g > 0);
+        tc_commit_warp(bar(W_DPFULL));
+      };
+      bool ok = mbar_wait_warp(bar(W_AB), 0, limit) && mbar_wait_warp(bar(W_QFULL), 0, limit);
+      tc_fence_after();
+      if (ok) s_mma(0);
+      ok = ok && mbar_wait_warp(bar(W_OFULL), 0, limit);
+      tc_fence_after();
+      if (ok) dp_mma(0);
+      for (int i = 0; ok && i < n; ++i) {
+        const int nx = i + 1;
+        // dV += P^T dO_i, 64 queries at a time
+        const uint64_t dg = desc64(sw128_desc(sG(i), L::kBox, 1024));
+        if (!(ok = mbar_wait_warp(bar(W_P), i & 1, limit))) break;
+        tc_fence_after();
+        mma4_ts_warp(tbase + kTDV, tbase + kTS, dg, kIdescD, i > 0);
+        if (!(ok = mbar_wait_warp(bar(W_P + 1), i & 1, limit))) break;
+        tc_fence_after();
+        mma4_ts_warp(tbase + kTDV, tbase + kTS + 64, dg + 512, kIdescD, 1u);
+        tc_commit_warp(bar(W_OEMPTY + (i & 1)));
+        if (nx < n) {
+          if (!(ok = mbar_wait_warp(bar(W_QFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+          tc_fence_after();
+          s_mma(nx);
+        }
+        // dK += dS^T Q_i
+        const uint64_t dq = desc64(sw128_desc(sQ(i), L::kBox, 1024));
+        if (!(ok = mbar_wait_warp(bar(W_DS), i & 1, limit))) break;
+        tc_fence_after();
+        mma4_ts_warp(tbase + kTDK, tbase + kTDP, dq, kIdescD, i > 0);
+        if (!(ok = mbar_wait_warp(bar(W_DS + 1), i & 1, limit))) break;
+        tc_fence_after();
+        mma4_ts_warp(tbase + kTDK, tbase + kTDP + 64, dq + 512, kIdescD, 1u);
+        tc_commit_warp(bar(W_QEMPTY + (i & 1)));
+        if (nx < n) {
+          if (!(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+          tc_fence_after();
+          dp_mma(nx);
+        }
+      }
+      tc_commit_warp(bar(W_FINAL));
+      mbar_wait_warp(bar(W_FINAL), 0, limit);
+    }
+  } else if (warp >= 4) {
+    const int g = (warp - 4) >> 2;                      // columns 64 g .. 64 g + 63
+    const int r = (threadIdx.x - 128) & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t tS = tbase + lane_off + kTS + 64 * g, tDP = tbase + lane_off + kTDP + 64 * g;
+    const int fk = p.fbits != nullptr ? min(kt * 128 + r, p.N - 1) / p.P : 0;
+    const uint64_t sl2p = f2pack(p.sl2, p.sl2);
+    bool ok = true;
+    int e_next = n > 0 ? ld_pinned_s32(lst) : 0;
+    for (int i = 0; ok && i < n; ++i) {
+      const int e = e_next;
+      if (i + 1 < n) e_next = ld_pinned_s32(lst + i + 1);
+      const bool part = (e & kPartialBit) != 0 && p.fbits != nullptr;
+      uint32_t mw[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (part) query_mask(p, fk, (e & ~kPartialBit) * 128 + 64 * g, mw);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_QFULL + (i & 1)), (i >> 1) & 1, limit) &&
+                                       mbar_wait(bar(W_SFULL), i & 1, limit));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t rowv = sRow(i) + 256 * g;
+      uint32_t sr[64];
+      float* pv = reinterpret_cast<float*>(sr);
+      tmem_ld_x64(tS, sr);
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 nl = ld_shared_f4(rowv + 4 * c);
+        const uint64_t x01 = ffma2(f2pack(pv[c], pv[c + 1]), sl2p, f2pack(nl.x, nl.y));
+        const uint64_t x23 = ffma2(f2pack(pv[c + 2], pv[c + 3]), sl2p, f2pack(nl.z, nl.w));
+        float x0, x1, x2, x3;
+        f2unpack(x01, x0, x1);
+        f2unpack(x23, x2, x3);
+        pv[c] = ex2_approx(x0);
+        pv[c + 1] = ex2_approx(x1);
+        pv[c + 2] = ex2_approx(x2);
+        pv[c + 3] = ex2_approx(x3);
+        if (part) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (!((mw[(c + u) >> 5] >> ((c + u) & 31)) & 1u)) pv[c + u] = 0.f;
+        }
+        pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
+        pk[c / 2 + 1] = pack_bf16x2(pv[c + 2], pv[c + 3]);
+      }
+      tmem_st_x32(tS, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(W_P + g));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_DPFULL), i & 1, limit));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dr[64];
+      const float* dv = reinterpret_cast<const float*>(dr);
+      tmem_ld_x64(tDP, dr);
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 nd = ld_shared_f4(rowv + 512 + 4 * c);
+        const uint64_t y01 = fmul2(f2pack(pv[c], pv[c + 1]), fadd2(f2pack(dv[c], dv[c + 1]), f2pack(nd.x, nd.y)));
+        const uint64_t y23 =
+            fmul2(f2pack(pv[c + 2], pv[c + 3]), fadd2(f2pack(dv[c + 2], dv[c + 3]), f2pack(nd.z, nd.w)));
+        float y0, y1, y2, y3;
+        f2unpack(y01, y0, y1);
+        f2unpack(y23, y2, y3);
+        pk[c / 2] = pack_bf16x2(y0, y1);
+        pk[c / 2 + 1] = pack_bf16x2(y2, y3);
+      }
+      tmem_st_x32(tDP, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(W_DS + g));
+    }
+    // epilogue: group 0 writes dV (through V's tile), group 1 dK (through K's)
+    if (n > 0) {
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(W_FINAL), 0, limit));
+      tc_fence_after();
+      mbar_wait(bar(W_AB), 0, limit);                   // the tile has landed before it is written over
+    }
+    const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
+    const uint32_t sOut = base + (g ? L::kA : L::kB);
+    store_rows<D>(tbase + lane_off + (g ? kTDK : kTDV), sOut, r, g ? p.scale : 1.f, have);
+    fence_proxy_async_smem();
+    named_barrier_sync(1 + g, 128);
+    if (r == 0) {
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) tma_store_3d(g ? &tmDK : &tmDV, sOut + b * L::kBox, b * 64, h, kt * 128);
+      bulk_commit();
+      bulk_wait_read_all();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+enum : int { X_AB = 0, X_KFULL = 1, X_KEMPTY = 4, X_VFULL = 7, X_VEMPTY = 9, X_SFULL = 11, X_DPFULL = 13, X_DS = 14, X_FINAL = 16 };
+
+// dQ of one query tile.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                   const __grid_constant__ CUtensorMap tmDQ, const BwdParams p) {
+  using L = BwdSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t bar0 = base + L::kBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + L::kHolder);
+
+  const int qt = blockIdx.x, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = p.wait_limit_ns;
+  const int NP = p.nB * 128;
+  int m = p.count[static_cast<size_t>(h) * p.chs + qt];       // entries; n: those in range
+  m = min(max(m, 0), p.lrs);
+  const size_t off = static_cast<size_t>(h) * p.lhs + static_cast<size_t>(qt) * p.lrs;
+  const int32_t* lst = p.list + off;
+  const uint8_t* flg = p.flags != nullptr ? p.flags + off : nullptr;
+  int n = 0;
+  for (int j0 = 0; j0 < m; j0 += 32) {
+    const int e = j0 + lane < m ? lst[j0 + lane] : -1;
+    n += __popc(__ballot_sync(0xFFFFFFFFu, e >= 0 && e < p.nB));
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i <= X_FINAL; ++i) mbar_init(bar(i), (i >= X_DS && i < X_FINAL) ? 4 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + L::kHolder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *holder;
+  constexpr uint32_t kTDP = 256, kTDQ = 384;                  // S_0 at 0, S_1 at 128
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdescD = idesc_bf16_f32(128, D, false, true);
+  auto sK = [&](int j) -> uint32_t { return base + L::kRing + (j % 3) * L::kTile; };
+  auto sV = [&](int j) -> uint32_t { return base + L::kRing + (3 + (j & 1)) * L::kTile; };
+
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(bar(X_AB), 2 * L::kTile);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        tma_load_3d(base + L::kA + b * L::kBox, &tmQ, bar(X_AB), b * 64, h, qt * 128);
+        tma_load_3d(base + L::kB + b * L::kBox, &tmG, bar(X_AB), b * 64, h, qt * 128);
+      }
+      int jk = 0, jv = 0;
+      bool ok = true;
+      for (int u = 0; u < m; ++u) {
+        const int kt = lst[u];
+        if (kt < 0 || kt >= p.nB) continue;
+        if (jk >= 3) ok = mbar_wait(bar(X_KEMPTY + jk % 3), (jk / 3 - 1) & 1, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(X_KFULL + jk % 3), L::kTile);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(sK(jk) + b * L::kBox, &tmK, bar(X_KFULL + jk % 3), b * 64, h, kt * 128);
+        ++jk;
+        if (jv >= 2) ok = mbar_wait(bar(X_VEMPTY + (jv & 1)), ((jv >> 1) - 1) & 1, limit);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(X_VFULL + (jv & 1)), L::kTile);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(sV(jv) + b * L::kBox, &tmV, bar(X_VFULL + (jv & 1)), b * 64, h, kt * 128);
+        ++jv;
+      }
+      mbar_wait(bar(X_AB), 0, limit);
+      for (int u = max(0, jk - 3); u < jk; ++u) mbar_wait(bar(X_KFULL + u % 3), (u / 3) & 1, limit);
+      for (int u = max(0, jv - 2); u < jv; ++u) mbar_wait(bar(X_VFULL + (u & 1)), (u >> 1) & 1, limit);
+    }
+  } else if (warp == 1) {
+    if (n > 0) {
+      const uint64_t dQ = desc64(sw128_desc(base + L::kA, 16, 1024)), dG = desc64(sw128_desc(base + L::kB, 16, 1024));
+      // S = Q K_j^T into buffer j % 2
+      auto s_mma = [&](int j) {
+        const uint64_t dk = desc64(sw128_desc(sK(j), 16, 1024));
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+          mma4_ss_warp(tbase + (j & 1) * 128, dQ + g * (L::kBox >> 4), dk + g * (L::kBox >> 4), kIdescS, g > 0);
+        tc_commit_warp(bar(X_SFULL + (j & 1)));
+      };
+      // dP = dO V_j^T; V_j is free after it
+      auto dp_mma = [&](int j) {
+        const uint64_t dv = desc64(sw128_desc(sV(j), 16, 1024));
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+          mma4_ss_warp(tbase + kTDP, dG + g * (L::kBox >> 4), dv + g * (L::kBox >> 4), kIdescS, g > 0);
+        tc_commit2_warp(bar(X_DPFULL), bar(X_VEMPTY + (j & 1)));
+      };
+      auto k_wait = [&](int j) -> bool {
+        const bool w = mbar_wait_warp(bar(X_KFULL + j % 3), (j / 3) & 1, limit);
+        tc_fence_after();
+        return w;
+      };
+      auto v_wait = [&](int j) -> bool {
+        const bool w = mbar_wait_warp(bar(X_VFULL + (j & 1)), (j >> 1) & 1, limit);
+        tc_fence_after();
+        return w;
+      };
+      bool ok = mbar_wait_warp(bar(X_AB), 0, limit) && k_wait(0);
+      if (ok) s_mma(0);
+      ok = ok && v_wait(0);
+      if (ok) dp_mma(0);
+      if (ok && n > 1 && (ok = k_wait(1))) s_mma(1);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n && !(ok = v_wait(j + 1))) break;
+        // dS_j of both halves: dP has been read and S_j is done with
+        const uint64_t dk = desc64(sw128_desc(sK(j), L::kBox, 1024));
+        const uint32_t tA = tbase + (j & 1) * 128;
+        if (!(ok = mbar_wait_warp(bar(X_DS), j & 1, limit))) break;
+        if (!(ok = mbar_wait_warp(bar(X_DS + 1), j & 1, limit))) break;
+        tc_fence_after();
+        if (j + 1 < n) dp_mma(j + 1);
+        // dQ += dS K_j
+        mma4_ts_warp(tbase + kTDQ, tA, dk, kIdescD, j > 0);
+        mma4_ts_warp(tbase + kTDQ, tA + 64, dk + 512, kIdescD, 1u);
+        tc_commit_warp(bar(X_KEMPTY + j % 3));
+        if (j + 2 < n && (ok = k_wait(j + 2))) s_mma(j + 2);
+      }
+      tc_commit_warp(bar(X_FINAL));
+      mbar_wait_warp(bar(X_FINAL), 0, limit);
+    }
+  } else if (warp >= 4) {
+    const int g = (warp - 4) >> 2;
+    const int r = (threadIdx.x - 128) & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t tDP = tbase + lane_off + kTDP + 64 * g;
+    const int fq = p.fbits != nullptr ? min(qt * 128 + r, p.N - 1) / p.P : 0;
+    const float nl = p.nl[static_cast<size_t>(h) * NP + qt * 128 + r], nd = p.nd[static_cast<size_t>(h) * NP + qt * 128 + r];
+    const uint64_t sl2p = f2pack(p.sl2, p.sl2), nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
+    bool ok = true;
+    int j = 0;
+    int kt_next = m > 0 ? ld_pinned_s32(lst) : 0;
+    uint32_t f_next = (m > 0 && flg != nullptr) ? ld_pinned_u8(flg) : 0u;
+    for (int u = 0; ok && u < m; ++u) {
+      const int kt = kt_next;
+      const uint32_t fl = f_next;
+      if (u + 1 < m) {
+        kt_next = ld_pinned_s32(lst + u + 1);
+        if (flg != nullptr) f_next = ld_pinned_u8(flg + u + 1);
+      }
+      if (kt < 0 || kt >= p.nB) continue;
+      const bool part = flg != nullptr ? fl != 0u : kt * 128 + 128 > p.N;
+      uint32_t mw[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (part) key_mask(p, fq, kt * 128 + 64 * g, mw);
+      const uint32_t tS = tbase + lane_off + (j & 1) * 128 + 64 * g;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(X_SFULL + (j & 1)), (j >> 1) & 1, limit));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[64];
+      float* pv = reinterpret_cast<float*>(sr);
+      tmem_ld_x64(tS, sr);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float x0, x1;
+        f2unpack(ffma2(f2pack(pv[c], pv[c + 1]), sl2p, nlp), x0, x1);
+        pv[c] = ex2_approx(x0);
+        pv[c + 1] = ex2_approx(x1);
+      }
+      if (part) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (!((mw[c >> 5] >> (c & 31)) & 1u)) pv[c] = 0.f;
+      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(X_DPFULL), j & 1, limit));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dr[64], pk[32];
+      const float* dv = reinterpret_cast<const float*>(dr);
+      tmem_ld_x64(tDP, dr);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float y0, y1;
+        f2unpack(fmul2(f2pack(pv[c], pv[c + 1]), fadd2(f2pack(dv[c], dv[c + 1]), ndp)), y0, y1);
+        pk[c / 2] = pack_bf16x2(y0, y1);
+      }
+      tmem_st_x32(tS, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(X_DS + g));
+      ++j;
+    }
+    // epilogue: each group writes half of dQ's channels through Q's tile
+    if (n > 0) {
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(X_FINAL), 0, limit));
+      tc_fence_after();
+      mbar_wait(bar(X_AB), 0, limit);
+    }
+    const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
+    if (D == 128 || g == 0) {
+      const uint32_t sOut = base + L::kA + g * L::kBox;
+      store_rows<64>(tbase + lane_off + kTDQ + 64 * g, sOut, r, p.scale, have);
+      fence_proxy_async_smem();
+      named_barrier_sync(1 + g, 128);
+      if (r == 0) {
+        tma_store_3d(&tmDQ, sOut, g * 64, h, qt * 128);
+        bulk_commit();
+        bulk_wait_read_all();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+}  // namespace bsa

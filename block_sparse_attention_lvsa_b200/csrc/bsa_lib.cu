@@ -19,6 +19,7 @@
 #include "blockmass.cuh"
 #include "rope.cuh"
 #include "blockmean.cuh"
+#include "attn_bwd.cuh"
 
 namespace {
 
@@ -173,6 +174,34 @@ size_t index_ws_bytes(const bsa_index* index, int N, int H) {
   return t;
 }
 
+// Workspace of the attention's gradient: the index's own part, the padded
+// per-row values, the bit sets of the lists and the lists the other way round
+// (shared by all heads for LVSA frame indexes).
+struct BwdWs {
+  size_t nl, nd, bits, part, tcnt, tlist, total;
+  int lists;                        // heads with lists of their own (1: shared)
+};
+BwdWs bwd_ws_layout(const bsa_index* index, int N, int H) {
+  BwdWs w;
+  std::memset(&w, 0, sizeof(w));
+  const size_t ix = index_ws_bytes(index, N, H);
+  if (ix == static_cast<size_t>(-1)) {
+    w.total = ix;
+    return w;
+  }
+  const size_t nB = static_cast<size_t>(n_tiles(N)), nW = (nB + 31) / 32;
+  const size_t lists = index->kind == BSA_INDEX_LVSA_FRAMES ? 1 : static_cast<size_t>(H);
+  w.lists = static_cast<int>(lists);
+  w.nl = round_up(ix, 256);
+  w.nd = w.nl + static_cast<size_t>(H) * nB * 128 * 4;
+  w.bits = w.nd + static_cast<size_t>(H) * nB * 128 * 4;
+  w.part = round_up(w.bits + lists * nW * nB * 4, 256);
+  w.tcnt = index->kind == BSA_INDEX_BLOCKS ? w.part : round_up(w.part + lists * nW * nB * 4, 256);
+  w.tlist = round_up(w.tcnt + lists * nB * 4, 256);
+  w.total = round_up(w.tlist + lists * nB * nB * 4, 256);
+  return w;
+}
+
 // Validates `index`, enqueues its expansion (LVSA frame sets -> tile lists,
 // flags of the intersection) and fills the list fields of `p`; *used = the
 // workspace bytes taken from its start.
@@ -283,6 +312,7 @@ size_t bsa_workspace_bytes(int op, int N, int H, int d, const bsa_index* index) 
   // head shares of log partial sums: every head in one pass, up to 4 GiB
   const size_t heads = std::max<size_t>(1, std::min<size_t>(static_cast<size_t>(H), (size_t(4) << 30) / per_head));
   if (op == BSA_OP_DENSE_BLOCKMASS) return per_head * heads;
+  if (op == BSA_OP_BLOCKSPARSE_BWD) return bwd_ws_layout(index, N, H).total;
   if (op != BSA_OP_BLOCKSPARSE_FWD && op != BSA_OP_BLOCKMASS) return static_cast<size_t>(-1);
   const size_t ix = index_ws_bytes(index, N, H);
   if (ix == static_cast<size_t>(-1)) return ix;
@@ -780,3 +810,116 @@ int blockmean_select(const void* q, const void* k, int N, int H, int d, int bloc
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Gradient of the block-sparse attention.
+namespace {
+
+template <int D>
+int launch_bwd(const void* go, const void* q, const void* k, const void* v, int N, int H, const BwdParams& p,
+               void* dq, void* dk, void* dv, cudaStream_t st) {
+  static std::atomic<bool> done_kv[kMaxDevices], done_q[kMaxDevices];
+  int rc = allow_smem(attn_bwd_dkv_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done_kv);
+  if (rc == BSA_OK) rc = allow_smem(attn_bwd_dq_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done_q);
+  if (rc != BSA_OK) return rc;
+  CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
+  if (!make_qkv_map(&mq, q, N, H, D, 128) || !make_qkv_map(&mk, k, N, H, D, 128) ||
+      !make_qkv_map(&mv, v, N, H, D, 128) || !make_qkv_map(&mg, go, N, H, D, 128) ||
+      !make_qkv_map(&mdq, dq, N, H, D, 128) || !make_qkv_map(&mdk, dk, N, H, D, 128) ||
+      !make_qkv_map(&mdv, dv, N, H, D, 128))
+    return BSA_ERR_CUDA;
+  const dim3 grid(p.nB, H);
+  attn_bwd_dkv_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdk, mdv, p);
+  attn_bwd_dq_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" int blocksparse_attn_bwd(const void* go, const void* q, const void* k, const void* v, const bsa_heads* o,
+                                    const float* lse, int N, int H, int d, float scale, const bsa_index* index,
+                                    void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_qkv(q, k, v, N, H, d, go, lse);
+  if (rc != BSA_OK) return rc;
+  if (!dq || !dk || !dv || !index || !std::isfinite(scale) || !(scale > 0.f)) return BSA_ERR_ARG;
+  if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16)) return BSA_ERR_ARG;
+  if ((rc = check_heads(o, BSA_BF16, N, d, false)) != BSA_OK) return rc;
+  if (o->H != H) return BSA_ERR_SHAPE;
+  const size_t bytes = static_cast<size_t>(N) * H * d * 2;
+  const size_t obytes = (static_cast<size_t>(N - 1) * o->token_stride + static_cast<size_t>(H - 1) * o->head_stride + d) * 2;
+  const void* outs[3] = {dq, dk, dv};
+  const void* ins[4] = {go, q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(outs[i], bytes, ins[j], bytes)) return BSA_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], bytes, outs[j], bytes)) return BSA_ERR_ARG;
+    if (overlap(outs[i], bytes, o->data, obytes)) return BSA_ERR_ARG;
+    if (overlap(outs[i], bytes, lse, static_cast<size_t>(H) * N * 4)) return BSA_ERR_ARG;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  AttnParams a = base_params(N, H, scale, nullptr, nullptr);
+  const BwdWs w = bwd_ws_layout(index, N, H);
+  size_t used = 0;
+  // what setup_index enqueues must fit too: check the whole workspace first
+  if (w.total != static_cast<size_t>(-1) && (!workspace || !aligned(workspace, 256) || ws_bytes < w.total)) {
+    const bool blocks = index->kind == BSA_INDEX_BLOCKS || index->kind == BSA_INDEX_LVSA_BLOCKS;
+    if (blocks && index->block != 128) return BSA_ERR_UNSUPPORTED;
+    if (blocks && (index->H != H || index->nQB != a.nB || index->nKB != a.nB)) return BSA_ERR_SHAPE;
+    return BSA_ERR_WORKSPACE;
+  }
+  rc = setup_index(index, N, H, workspace, ws_bytes, a, &used, st);
+  if (rc != BSA_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int nB = a.nB, nW = (nB + 31) / 32;
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = N;
+  p.H = H;
+  p.nB = nB;
+  p.sl2 = a.sl2;
+  p.scale = scale;
+  p.list = a.list;
+  p.count = a.count;
+  p.flags = a.flags;
+  p.lhs = a.lhs;
+  p.lrs = a.lrs;
+  p.chs = a.chs;
+  p.fbits = a.fbits;
+  p.TW = a.TW;
+  p.P = a.P;
+  p.wait_limit_ns = a.wait_limit_ns;
+  float* nl = reinterpret_cast<float*>(ws + w.nl);
+  float* nd = reinterpret_cast<float*>(ws + w.nd);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(ws + w.bits);
+  uint32_t* part = a.flags ? reinterpret_cast<uint32_t*>(ws + w.part) : nullptr;
+  int32_t* tcnt = reinterpret_cast<int32_t*>(ws + w.tcnt);
+  int32_t* tlist = reinterpret_cast<int32_t*>(ws + w.tlist);
+  p.nl = nl;
+  p.nd = nd;
+  p.tlist = tlist;
+  p.tcount = tcnt;
+  p.tlhs = w.lists == 1 ? 0 : static_cast<long long>(nB) * nB;
+  p.tchs = w.lists == 1 ? 0 : nB;
+  attn_bwd_bits_kernel<<<dim3((nB + 3) / 4, w.lists), 128, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB,
+                                                                   bits, part);
+  attn_bwd_lists_kernel<<<dim3((nW + 3) / 4, w.lists), 128, 0, st>>>(nB, bits, part, tlist, tcnt);
+  const long long lanes = static_cast<long long>(nB) * 128 * H * (d / 8);
+  const unsigned blocks = static_cast<unsigned>((lanes + 255) / 256);
+  const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o->data);
+  const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(go);
+  if (d == 128)
+    attn_bwd_rows_kernel<128><<<blocks, 256, 0, st>>>(ob, o->token_stride, o->head_stride, gb, lse, N, H, nB * 128,
+                                                    nl, nd);
+  else
+    attn_bwd_rows_kernel<64><<<blocks, 256, 0, st>>>(ob, o->token_stride, o->head_stride, gb, lse, N, H, nB * 128,
+                                                    nl, nd);
+  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+  return d == 128 ? launch_bwd<128>(go, q, k, v, N, H, p, dq, dk, dv, st)
+                  : launch_bwd<64>(go, q, k, v, N, H, p, dq, dk, dv, st);
+}

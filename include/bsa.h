@@ -297,34 +297,6 @@ int blocksparse_attn_fwd_noalloc(const void* q, const void* k, const void* v,
                                  const bsa_index* index, void* o, float* lse,
                                  void* stream);
 
-/*
- * blockmean_select - per (head, query block) the key blocks of the largest
- * mean score, for the block-sparse attention.
- *
- * For 128-token blocks i of q and j of k (the last one may be short), per head
- *   s(i, j) = < mean of q over block i, mean of k over block j >,
- * the mean of the tile's scores <q, k>.  Row i keeps its neighbourhood
- * |i - j| <= local and then the blocks of the largest s, at equal scores the
- * lower j first, until it holds max(min(keep, nB), size of the neighbourhood)
- * blocks; the list is written ascending.  Means and deciding scores are
- * computed in 64 bits; a score that is not a number counts as the lowest.
- * Unlike losa_select this needs no dense step: q and k are read once.
- *
- * q, k: in, bf16 [N,H,d].  block: must be 128.  keep >= 1.  local >= -1 (-1:
- * no neighbourhood, 0: the own block).
- * idx: out, int32 [H][nB][nB], kept ids ascending, then -1 padding; cnt: out,
- * int32 [H][nB] (an index of kind BSA_INDEX_BLOCKS).
- * workspace: device, 256-byte aligned, at least
- * blockmean_select_workspace_bytes(N, H, d) bytes; overwritten.
- * Limits: ceil(N / 128) <= 8192.
- * Returns BSA_OK, BSA_WARN_OVER_BUDGET (some neighbourhood holds more than
- * `keep` blocks) or a negative bsa_status.
- */
-int blockmean_select(const void* q, const void* k, int N, int H, int d, int block, int keep, int local,
-                     int32_t* idx, int32_t* cnt, void* workspace, size_t ws_bytes, void* stream);
-/* Scratch bytes of blockmean_select; (size_t)-1 for invalid arguments. */
-size_t blockmean_select_workspace_bytes(int N, int H, int d);
-
 /* Element types of bsa_heads tensors and norm weights. */
 enum {
   BSA_BF16 = 0,
@@ -353,6 +325,66 @@ typedef struct bsa_heads {
   int H;
   long long token_stride, head_stride;
 } bsa_heads;
+
+/*
+ * blocksparse_attn_bwd - gradient of blocksparse_attn_fwd.
+ *
+ * For the gradient go of o, with p = exp(scale <q,k> - lse) over the pairs
+ * that `index` admits and D_q = <go_q, o_q>:
+ *   dv_k = sum_q p go_q,   ds = p (<go_q, v_k> - D_q),
+ *   dq_q = scale sum_k ds k_k,   dk_k = scale sum_q ds q_q.
+ * Sums in float32, the factors p and ds of the products and the outputs
+ * rounded to bfloat16.  No atomics: the result is the same from run to run.
+ * Queries without a key, and keys that no query attends, get 0.
+ *
+ * go, q, k, v: in, bf16 [N,H,d]; o: in, bf16 [N,H,d] by strides (a saved o may
+ * have been laid out anew); lse: in, float32 [H,N]; o and lse hold what the
+ * forward call returned for the same q, k, v, scale and index.  (lse is a
+ * constant here: a gradient of lse itself is not taken.)  All values of the
+ * listed tiles must be finite.  scale: finite, > 0 (the forward call finds the
+ * largest scaled score from the largest product, which needs a positive scale).
+ * index: any kind accepted by blocksparse_attn_fwd; the ids of a list must
+ * differ from one another.  Entries out of range are skipped; they and
+ * repeated ids are reported as BSA_ERR_INDEX_RANGE through the device status
+ * word (the gradients of a row with a repeated id are not defined).
+ * dq, dk, dv: out, bf16 [N,H,d], must not overlap the inputs or one another.
+ * workspace: device, 256-byte aligned, at least
+ * bsa_workspace_bytes(BSA_OP_BLOCKSPARSE_BWD, N, H, d, index) bytes;
+ * overwritten.  It holds the index's lists the other way round (the query
+ * tiles of every key tile).
+ * Returns BSA_OK or a negative bsa_status.
+ */
+int blocksparse_attn_bwd(const void* go, const void* q, const void* k, const void* v, const bsa_heads* o,
+                         const float* lse, int N, int H, int d, float scale, const bsa_index* index,
+                         void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * blockmean_select - per (head, query block) the key blocks of the largest
+ * mean score, for the block-sparse attention.
+ *
+ * For 128-token blocks i of q and j of k (the last one may be short), per head
+ *   s(i, j) = < mean of q over block i, mean of k over block j >,
+ * the mean of the tile's scores <q, k>.  Row i keeps its neighbourhood
+ * |i - j| <= local and then the blocks of the largest s, at equal scores the
+ * lower j first, until it holds max(min(keep, nB), size of the neighbourhood)
+ * blocks; the list is written ascending.  Means and deciding scores are
+ * computed in 64 bits; a score that is not a number counts as the lowest.
+ * Unlike losa_select this needs no dense step: q and k are read once.
+ *
+ * q, k: in, bf16 [N,H,d].  block: must be 128.  keep >= 1.  local >= -1 (-1:
+ * no neighbourhood, 0: the own block).
+ * idx: out, int32 [H][nB][nB], kept ids ascending, then -1 padding; cnt: out,
+ * int32 [H][nB] (an index of kind BSA_INDEX_BLOCKS).
+ * workspace: device, 256-byte aligned, at least
+ * blockmean_select_workspace_bytes(N, H, d) bytes; overwritten.
+ * Limits: ceil(N / 128) <= 8192.
+ * Returns BSA_OK, BSA_WARN_OVER_BUDGET (some neighbourhood holds more than
+ * `keep` blocks) or a negative bsa_status.
+ */
+int blockmean_select(const void* q, const void* k, int N, int H, int d, int block, int keep, int local,
+                     int32_t* idx, int32_t* cnt, void* workspace, size_t ws_bytes, void* stream);
+/* Scratch bytes of blockmean_select; (size_t)-1 for invalid arguments. */
+size_t blockmean_select_workspace_bytes(int N, int H, int d);
 
 /*
  * Rotary positions over up to three axes (time, height, width); host struct,
@@ -454,7 +486,8 @@ size_t qk_norm_rope_bwd_workspace_bytes(long long N, int Hq, int Hk, int d);
 enum {
   BSA_OP_BLOCKSPARSE_FWD = 1,
   BSA_OP_DENSE_BLOCKMASS = 2,
-  BSA_OP_BLOCKMASS = 3
+  BSA_OP_BLOCKMASS = 3,
+  BSA_OP_BLOCKSPARSE_BWD = 4
 };
 
 /*

@@ -760,19 +760,89 @@ int allow_smem(K* kernel, int bytes, std::atomic<bool>* done) {
   return BSA_OK;
 }
 
-constexpr int kMeanSelectSmem = 96 * 1024;            // keys of all warps of a block
+// Workspace: means (64-bit), norms, the two bf16 parts, rough scores of the
+// heads of one pass.
+struct MeanWs {
+  size_t mean, norm, hi, lo, scores, total;
+  size_t per_head;                  // scores of one head
+  int ldS;                          // floats per row of scores
+  int heads;                        // heads per pass
+};
+// Scores of one pass: small enough to stay in L2 (126 MB) between the kernel
+// that writes them and the one that reads them.
+constexpr size_t kMeanPassBytes = size_t(64) << 20;
+
+MeanWs mean_ws_layout(int N, int H, int d) {
+  const size_t nB = static_cast<size_t>(n_tiles(N)), elems = static_cast<size_t>(2) * H * nB * d;
+  MeanWs w;
+  w.ldS = static_cast<int>(round_up(nB, 4));
+  w.per_head = nB * w.ldS * 4;
+  w.heads = static_cast<int>(std::max<size_t>(1, std::min<size_t>(H, kMeanPassBytes / w.per_head)));
+  w.mean = 0;
+  w.norm = elems * 8;
+  w.hi = round_up(w.norm + static_cast<size_t>(2) * H * nB * 8, 256);
+  w.lo = round_up(w.hi + elems * 2, 256);
+  w.scores = round_up(w.lo + elems * 2, 256);
+  w.total = round_up(w.scores + w.per_head * w.heads, 256);
+  return w;
+}
+
+bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, int es, const void* ptr, cuuint64_t x, cuuint64_t y,
+                 cuuint64_t z, cuuint64_t pitch, cuuint32_t bx) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {x, y, z};
+  cuuint64_t strides[2] = {pitch * es, y * pitch * es};
+  cuuint32_t box[3] = {bx, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMeanSelectSmem = 160 * 1024;           // keys (and long rows) of all warps of a block
+
+template <int D, int KPL>
+int launch_mean_select(const MeanWs& w, const uint8_t* ws, int H, int h0, int heads, int nB, int keep, int local,
+                       int32_t* idx, int32_t* cnt, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  int rc = allow_smem(blockmean_select_kernel<D, KPL>, kMeanSelectSmem, done);
+  if (rc != BSA_OK) return rc;
+  const size_t per_warp = (static_cast<size_t>(nB) + (KPL == 0 ? (nB + 1) / 2 : 0)) * 8;
+  const int wpc = static_cast<int>(std::min<size_t>(kSelWarps, std::max<size_t>(1, kMeanSelectSmem / per_warp)));
+  const dim3 grid((nB + wpc - 1) / wpc, heads);
+  blockmean_select_kernel<D, KPL><<<grid, wpc * 32, wpc * per_warp, st>>>(
+      reinterpret_cast<const double*>(ws + w.mean), reinterpret_cast<const double*>(ws + w.norm),
+      reinterpret_cast<const float*>(ws + w.scores), w.ldS, H, h0, nB, keep, local, idx, cnt);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
 
 template <int D>
-int launch_mean_select(const double* mean, int H, int nB, int keep, int local, int32_t* idx, int32_t* cnt,
-                       cudaStream_t st) {
+int launch_mean(const MeanWs& w, uint8_t* ws, int H, int nB, int keep, int local, int32_t* idx, int32_t* cnt,
+                cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  int rc = allow_smem(blockmean_select_kernel<D>, kMeanSelectSmem, done);
+  int rc = allow_smem(blockmean_score_kernel<D>, static_cast<int>(ScoreSmem<D>::kAlloc), done);
   if (rc != BSA_OK) return rc;
-  const int wpc = std::min(8, std::max(1, kMeanSelectSmem / (nB * 8)));
-  const dim3 grid((nB + wpc - 1) / wpc, H);
-  blockmean_select_kernel<D><<<grid, wpc * 32, static_cast<size_t>(wpc) * nB * 8, st>>>(mean, H, nB, keep, local, idx,
-                                                                                     cnt);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  CUtensorMap mh, ml;
+  if (!make_map_3d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ws + w.hi, D, nB, 2ull * H, D, 64) ||
+      !make_map_3d(&ml, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ws + w.lo, D, nB, 2ull * H, D, 64))
+    return BSA_ERR_CUDA;
+  const unsigned tiles = static_cast<unsigned>((nB + 127) / 128);
+  for (int h0 = 0; h0 < H; h0 += w.heads) {
+    const int hn = std::min(w.heads, H - h0);
+    CUtensorMap ms;
+    if (!make_map_3d(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + w.scores, nB, nB, hn, w.ldS, 32)) return BSA_ERR_CUDA;
+    blockmean_score_kernel<D><<<dim3(tiles, tiles, hn), kScoreThreads, ScoreSmem<D>::kAlloc, st>>>(mh, ml, ms, H, h0, nB,
+                                                                                              kWaitLimitNs);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+    if (nB <= 256) rc = launch_mean_select<D, 8>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 512) rc = launch_mean_select<D, 16>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 1024) rc = launch_mean_select<D, 32>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 2048) rc = launch_mean_select<D, 64>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else rc = launch_mean_select<D, 0>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    if (rc != BSA_OK) return rc;
+  }
+  return BSA_OK;
 }
 
 }  // namespace
@@ -780,30 +850,32 @@ int launch_mean_select(const double* mean, int H, int nB, int keep, int local, i
 extern "C" {
 
 size_t blockmean_select_workspace_bytes(int N, int H, int d) {
-  if (N < 1 || H < 1 || H > 65535 || (d != 64 && d != 128) || n_tiles(N) > kMeanMaxBlocks)
+  if (N < 1 || H < 1 || H > 32767 || (d != 64 && d != 128) || n_tiles(N) > kMeanMaxBlocks)
     return static_cast<size_t>(-1);
-  return round_up(static_cast<size_t>(2) * H * n_tiles(N) * d * sizeof(double), 256);
+  return mean_ws_layout(N, H, d).total;
 }
 
 int blockmean_select(const void* q, const void* k, int N, int H, int d, int block, int keep, int local, int32_t* idx,
                      int32_t* cnt, void* workspace, size_t ws_bytes, void* stream) {
   if (!q || !k || !idx || !cnt || !aligned(q, 16) || !aligned(k, 16) || !aligned(idx, 4) || !aligned(cnt, 4))
     return BSA_ERR_ARG;
-  if (N < 1 || H < 1 || H > 65535 || keep < 1 || local < -1) return BSA_ERR_ARG;
-  if (block != 128 || (d != 64 && d != 128)) return BSA_ERR_UNSUPPORTED;
+  if (N < 1 || H < 1 || keep < 1 || local < -1) return BSA_ERR_ARG;
+  if (block != 128 || (d != 64 && d != 128) || H > 32767) return BSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * H * d >= (1LL << 31) || n_tiles(N) > kMeanMaxBlocks) return BSA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 256) || ws_bytes < blockmean_select_workspace_bytes(N, H, d))
-    return BSA_ERR_WORKSPACE;
+  const MeanWs w = mean_ws_layout(N, H, d);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < w.total) return BSA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int nB = n_tiles(N);
   local = std::min(local, nB);
-  double* mean = static_cast<double*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   const dim3 grid(nB, (H * d + 255) / 256, 2);
-  blockmean_pool_kernel<<<grid, kPoolThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(q),
-                                                       static_cast<const __nv_bfloat16*>(k), N, H, d, nB, mean);
+  blockmean_pool_kernel<<<grid, kPoolThreads, 0, st>>>(
+      static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), N, H, d, nB,
+      reinterpret_cast<double*>(ws + w.mean), reinterpret_cast<__nv_bfloat16*>(ws + w.hi),
+      reinterpret_cast<__nv_bfloat16*>(ws + w.lo), reinterpret_cast<double*>(ws + w.norm));
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  const int rc = d == 128 ? launch_mean_select<128>(mean, H, nB, keep, local, idx, cnt, st)
-                          : launch_mean_select<64>(mean, H, nB, keep, local, idx, cnt, st);
+  const int rc = d == 128 ? launch_mean<128>(w, ws, H, nB, keep, local, idx, cnt, st)
+                          : launch_mean<64>(w, ws, H, nB, keep, local, idx, cnt, st);
   if (rc != BSA_OK) return rc;
   // the widest neighbourhood of any row
   return std::min<long long>(nB, 2LL * local + 1) > keep ? BSA_WARN_OVER_BUDGET : BSA_OK;

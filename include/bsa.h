@@ -377,7 +377,7 @@ int blocksparse_attn_bwd(const void* go, const void* q, const void* k, const voi
  * int32 [H][nB] (an index of kind BSA_INDEX_BLOCKS).
  * workspace: device, 256-byte aligned, at least
  * blockmean_select_workspace_bytes(N, H, d) bytes; overwritten.
- * Limits: ceil(N / 128) <= 8192.
+ * Limits: ceil(N / 128) <= 8192, H <= 32767.
  * Returns BSA_OK, BSA_WARN_OVER_BUDGET (some neighbourhood holds more than
  * `keep` blocks) or a negative bsa_status.
  */

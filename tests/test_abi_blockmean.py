@@ -24,8 +24,8 @@ def test_arguments(bsa):
 
     assert call(q=nul) == A and call(k=nul) == A and call(idx=nul) == A and call(cnt=nul) == A
     assert call(q=ctypes.c_void_p(0x10008)) == A
-    assert call(N=0) == A and call(H=0) == A and call(H=70000) == A and call(keep=0) == A and call(local=-2) == A
-    assert call(d=96) == U and call(block=64) == U
+    assert call(N=0) == A and call(H=0) == A and call(keep=0) == A and call(local=-2) == A
+    assert call(d=96) == U and call(N=1, H=40000) == U and call(block=64) == U
     assert call(N=128 * 8192 + 1, H=1) == U and call(N=1 << 20, H=64) == U
     assert call(n=n - 1) == W and call(ws=nul) == W and call(ws=ctypes.c_void_p(0x10010)) == W
     none = ctypes.c_size_t(-1).value

@@ -34,12 +34,23 @@ constexpr int kMeanMaxBlocks = 8192;
 constexpr int kPoolThreads = 256;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
+// A finite bf16 times 2^-896 as a 64-bit float, by moving its bits: the sign,
+// and the exponent and significand 3 places down; the exponent then counts from
+// 1023 instead of 127, and zero and subnormals stay what they are.  `w`: the
+// bf16 in the upper half of a word.  (The conversion instruction runs at a
+// fraction of the adds' rate and held the pooling at 4.6 TB/s; with the move it
+// reads NEW TB/s.)
+__device__ __forceinline__ double moved(uint32_t w) {
+  return __hiloint2double(static_cast<int>((static_cast<int32_t>(w) >> 3) & 0x8FFFE000), 0);
+}
+
 // grid (nB, ceil(H * d / 256), 2): one 128-token block of 256 neighbouring
 // channels (whole heads) of q or k.  A warp reads 512 contiguous bytes per
 // token, 8 channels a lane; its 16 tokens are added in 64 bits in order, then
 // the eight warps' sums in order: bf16 values are 8 bits wide, so such a sum
 // is exact unless the block spans more than 2^38, and equal blocks always
-// give equal means.
+// give equal means.  Channels with a value that is not finite are added again
+// without the move.
 // mean: [2][H][nB][d] double; hi, lo: bf16 [2][H][nB][d]; norm: [2][H][nB] double.
 __global__ void __launch_bounds__(kPoolThreads) blockmean_pool_kernel(
     const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, int N, int H, int d, int nB,
@@ -61,13 +72,24 @@ __global__ void __launch_bounds__(kPoolThreads) blockmean_pool_kernel(
 #pragma unroll
     for (int t = 0; t < 16; ++t)
       v[t] = (warp * 16 + t < rows) ? __ldg(reinterpret_cast<const uint4*>(p + t * row)) : make_uint4(0, 0, 0, 0);
+    uint32_t big[4] = {0, 0, 0, 0};                   // largest magnitude bits of each channel
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
       const uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[2 * i] += static_cast<double>(__uint_as_float(w[i] << 16));
-        acc[2 * i + 1] += static_cast<double>(__uint_as_float(w[i] & 0xFFFF0000u));
+        big[i] = __vmaxu2(big[i], w[i] & 0x7FFF7FFFu);
+        acc[2 * i] += moved(w[i] << 16);
+        acc[2 * i + 1] += moved(w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      acc[i] *= 0x1p+896;
+      if (((big[i / 2] >> (16 * (i & 1))) & 0xFFFFu) >= 0x7F80u) {
+        acc[i] = 0.0;
+        for (int t = 0; t < 16 && warp * 16 + t < rows; ++t)
+          acc[i] += static_cast<double>(__bfloat162float(p[t * row + i]));
       }
     }
   }
@@ -214,93 +236,119 @@ __device__ __forceinline__ float warp_max_f(float v) {
   return v;
 }
 
-constexpr int kSelWarps = 4;
+// warps (rows) per block; four long rows fill shared memory
+__host__ __device__ constexpr int sel_warps(int c4) { return c4 ? 8 : 4; }
+constexpr int kSelKeys = 32;
 constexpr float kRoughError = 1.0f / 8192.0f;         // E / (|q| max |k|), see above
 
-// One warp per row (grid (groups of rows, heads of the pass)).  Lane l holds
-// the rough scores of blocks l, l + 32, ... in registers (KPL of them; KPL = 0:
-// rows of more than 2048 blocks stay in shared memory).  Shared memory per
-// warp: nB 64-bit keys of candidates and, for KPL = 0, nB floats.
-template <int D, int KPL>
-__global__ void __launch_bounds__(kSelWarps * 32)
+// One warp per row (grid (groups of rows, heads of the pass)).  Block j sits
+// in lane (j % 128) / 4, component j % 4 of chunk j / 128, so that a lane reads
+// four neighbouring scores at once; C4 chunks are kept in registers, because
+// the bisection reads them again and again (C4 = 0: rows of more than 2048
+// blocks, in shared memory).  One pass then turns the scores into a bit per
+// block (sure, candidate; 8 chunks a word); what follows loops over those words:
+// code that is unrolled over the row more often does not fit the instruction
+// cache.  A few candidates are ranked directly, a lane each; more than kSelKeys
+// (rows of equal scores) by bisection over their keys, which then lie in memory
+// that is the row's own: the rough scores, no longer needed, and the output
+// list, not yet written.
+template <int D, int C4>
+__global__ void __launch_bounds__(sel_warps(C4) * 32)
 blockmean_select_kernel(const double* __restrict__ mean, const double* __restrict__ norm,
-                        const float* __restrict__ scores, int ldS, int H, int h0, int nB, int keep, int local,
-                        int32_t* __restrict__ idx, int32_t* __restrict__ cnt) {
-  extern __shared__ unsigned long long s_mean_keys[];
-  __shared__ double s_max[kSelWarps];
+                        float* scores, int ldS, int H, int h0, int nB, int keep, int local, int32_t* idx,
+                        int32_t* __restrict__ cnt) {
+  extern __shared__ float4 s_rows[];
+  constexpr int kW = sel_warps(C4);
+  constexpr int kWords = C4 ? (C4 + 7) / 8 : kMeanMaxBlocks / 1024;
+  __shared__ uint32_t s_sure[kW][kWords][32], s_cand[kW][kWords][32];
+  __shared__ unsigned long long s_key[kW][kSelKeys];
+  __shared__ int s_at[kW][kSelKeys];
+  __shared__ uint32_t s_max[kW];
   constexpr int E2 = D / 64;                          // double2 of a mean per lane
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wpc = blockDim.x >> 5;
-  const int qb = blockIdx.x * wpc + warp, h = h0 + blockIdx.y;
-  // largest norm of the head's key means; one that is not finite shows as such
-  double kmax = 0.0;
-  bool kfin = true;
-  for (int j = threadIdx.x; j < nB; j += blockDim.x) {
-    const double x = norm[(static_cast<size_t>(H) + h) * nB + j];
-    kfin = kfin && isfinite(x);
-    kmax = x > kmax ? x : kmax;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double x = __shfl_xor_sync(kAll, kmax, o);
-    kmax = x > kmax ? x : kmax;
-  }
-  if (lane == 0) s_max[warp] = kmax;
-  kfin = __syncthreads_and(kfin);
-  for (int w = 0; w < wpc; ++w) kmax = s_max[w] > kmax ? s_max[w] : kmax;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int qb = blockIdx.x * kW + warp, h = h0 + blockIdx.y;
+  // an upper bound of the head's key norms: the upper words of non-negative
+  // 64-bit floats order like them (not finite: above all others), plus one step
+  uint32_t top_word = 0;
+  const uint32_t* kn = reinterpret_cast<const uint32_t*>(norm + (static_cast<size_t>(H) + h) * nB);
+  for (int j = threadIdx.x; j < nB; j += kW * 32) top_word = max(top_word, kn[2 * j + 1]);
+  top_word = __reduce_max_sync(kAll, top_word);
+  if (lane == 0) s_max[warp] = top_word;
+  __syncthreads();
   if (qb >= nB) return;
+  for (int w = 0; w < kW; ++w) top_word = max(top_word, s_max[w]);
+  const bool kfin = top_word < 0x7FE00000u;
+  const double kmax = __hiloint2double(static_cast<int>(top_word + 1), 0);
 
-  const size_t per_warp = static_cast<size_t>(nB) + (KPL == 0 ? (nB + 1) / 2 : 0);
-  unsigned long long* key = s_mean_keys + warp * per_warp;
-  float* srow = reinterpret_cast<float*>(key + nB);
+  float4* srow = s_rows + static_cast<size_t>(warp) * (ldS / 4);
+  float* row = scores + (static_cast<size_t>(blockIdx.y) * nB + qb) * ldS;
+  int32_t* out = idx + (static_cast<size_t>(h) * nB + qb) * nB;
+  uint32_t(*sure)[32] = s_sure[warp];
+  uint32_t(*cand)[32] = s_cand[warp];
   const double* mq = mean + (static_cast<size_t>(h) * nB + qb) * D;
   const double* mk = mean + (static_cast<size_t>(H) + h) * nB * D;
-  const int chunks = KPL ? KPL : (nB + 31) / 32;
+  const int used = (nB + 127) / 128;                  // chunks
+  const int chunks = C4 ? C4 : used;
+  const int words = (used + 7) / 8;
   const int f0 = max(0, qb - local), f1 = local < 0 ? f0 : min(nB, qb + local + 1);   // own neighbourhood
   const int forced = f1 - f0, rest = nB - forced;
   const int take = min(nB, max(keep, forced)) - forced;        // blocks chosen by score
-
-  // rough scores; out of the choice: -infinity
-  float v[KPL ? KPL : 1];
-  float lo = INFINITY, hi = -INFINITY;
-  {
-    const float* row = scores + (static_cast<size_t>(blockIdx.y) * nB + qb) * ldS;
-#pragma unroll
-    for (int i = 0; i < chunks; ++i) {
-      const int j = i * 32 + lane;
-      const bool on = j < nB && (j < f0 || j >= f1);
-      const float x = on ? __ldg(row + j) : -INFINITY;
-      if (on) lo = fminf(lo, x);
-      hi = fmaxf(hi, x);
-      if (KPL) v[KPL ? i : 0] = x;
-      else if (j < nB) srow[j] = x;
-    }
-  }
-  lo = -warp_max_f(-lo);
-  hi = warp_max_f(hi);
-  __syncwarp();
-  auto score = [&](int i) -> float { return KPL ? v[KPL ? i : 0] : (i * 32 + lane < nB ? srow[i * 32 + lane] : -INFINITY); };
-  auto count = [&](float t) -> int {                  // blocks with a rough score >= t > -infinity
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < chunks; ++i) n += score(i) >= t ? 1 : 0;
-    return __reduce_add_sync(kAll, n);
-  };
-
-  // sure: kept for certain (> top); candidates: in [bottom, top]
-  float bottom = -INFINITY, top = INFINITY;
   const double qn = norm[static_cast<size_t>(h) * nB + qb], scale = qn * kmax;
   const bool choose = take > 0 && take < rest;
   const bool rough = choose && kfin && isfinite(qn) && qn >= 1e-25 && kmax >= 1e-25 && scale >= 1e-25 && scale <= 1e30;
+  auto own = [&](int j) -> bool { return j >= f0 && j < f1; };
+  // chunk i holds blocks that take no part in the choice
+  auto mixed = [&](int i) -> bool { return 128 * i + 128 > nB || (128 * i + 128 > f0 && 128 * i < f1); };
+
   if (rough) {
+    // rough scores; out of the choice: -infinity
+    float4 v[C4 ? C4 : 1];
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < chunks; ++i) {
+      const int j = 128 * i + 4 * lane;
+      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (j < nB) x = __ldcg(reinterpret_cast<const float4*>(row + j));
+      float mn;
+      if (mixed(i)) {
+        const bool a = j >= nB || own(j), b = j + 1 >= nB || own(j + 1), c = j + 2 >= nB || own(j + 2),
+                   e = j + 3 >= nB || own(j + 3);
+        mn = fminf(fminf(a ? INFINITY : x.x, b ? INFINITY : x.y), fminf(c ? INFINITY : x.z, e ? INFINITY : x.w));
+        x = make_float4(a ? -INFINITY : x.x, b ? -INFINITY : x.y, c ? -INFINITY : x.z, e ? -INFINITY : x.w);
+      } else {
+        mn = fminf(fminf(x.x, x.y), fminf(x.z, x.w));
+      }
+      lo = fminf(lo, mn);
+      hi = fmaxf(hi, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+      if (C4) v[C4 ? i : 0] = x;
+      else if (j < nB) srow[j / 4] = x;
+    }
+    lo = -warp_max_f(-lo);
+    hi = warp_max_f(hi);
+    __syncwarp();
+    auto score = [&](int i) -> float4 {
+      if (C4) return v[C4 ? i : 0];
+      if (128 * i + 4 * lane < nB) return srow[32 * i + lane];
+      return make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    };
     const float e = static_cast<float>(scale) * kRoughError;
-    // count(lo) >= take > count(hi): the take-th largest lies in [lo, hi)
+    // count(lo) >= take > count(hi), count(t) = blocks with a score >= t: the
+    // take-th largest lies in [lo, hi)
     int nlo = rest, nhi = 0;
     hi = hi + fmaxf(e, 1e-6f * fabsf(hi));
-    while (nlo - nhi > 1 && hi - lo > e) {
-      const float mid = lo + 0.5f * (hi - lo);
+    for (int step = 0; nlo - nhi > 1 && hi - lo > e; ++step) {
+      // by the counts' proportion, every third time in the middle
+      const float part = step % 3 == 2 ? 0.5f : (nlo - take + 0.5f) / (nlo - nhi);
+      const float mid = lo + fminf(fmaxf(part, 0.02f), 0.98f) * (hi - lo);
       if (!(mid > lo && mid < hi)) break;
-      const int n = count(mid);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < chunks; ++i) {
+        const float4 x = score(i);
+        n += (x.x >= mid ? 1 : 0) + (x.y >= mid ? 1 : 0) + (x.z >= mid ? 1 : 0) + (x.w >= mid ? 1 : 0);
+      }
+      n = __reduce_add_sync(kAll, n);
       if (n >= take) {
         lo = mid;
         nlo = n;
@@ -309,115 +357,169 @@ blockmean_select_kernel(const double* __restrict__ mean, const double* __restric
         nhi = n;
       }
     }
-    if (nlo - nhi == 1) {                             // the one score in [lo, hi)
-      float t = -INFINITY;
+    // the take-th largest rough score is within [lo, hi), the exact one within
+    // E of it
+    const float top = hi + 2.01f * e, bottom = lo - 2.01f * e;
+    uint32_t sm = 0, cm = 0;
 #pragma unroll
-      for (int i = 0; i < chunks; ++i) {
-        const float x = score(i);
-        if (x >= lo && x < hi) t = x;
+    for (int i = 0; i < chunks; ++i) {
+      const float4 x = score(i);
+      const int b = 4 * (i & 7);
+      sm |= (x.x > top ? 1u << b : 0u) | (x.y > top ? 2u << b : 0u) | (x.z > top ? 4u << b : 0u) | (x.w > top ? 8u << b : 0u);
+      cm |= (x.x >= bottom ? 1u << b : 0u) | (x.y >= bottom ? 2u << b : 0u) | (x.z >= bottom ? 4u << b : 0u) |
+            (x.w >= bottom ? 8u << b : 0u);
+      if ((i & 7) == 7 || i == chunks - 1) {
+        sure[i >> 3][lane] = sm;
+        cand[i >> 3][lane] = cm & ~sm;
+        sm = cm = 0;
       }
-      lo = hi = warp_max_f(t);
     }
-    top = hi + 2.01f * e;
-    bottom = lo - 2.01f * e;
+  } else {
+    // no rough scores: nothing is sure; when there is a choice every block
+    // outside the neighbourhood is weighed
+    for (int w = 0; w < words; ++w) {
+      uint32_t cm = 0;
+      for (int b = 0; b < 32; ++b) {
+        const int j = 128 * (8 * w + b / 4) + 4 * lane + b % 4;
+        if (choose && j < nB && !own(j)) cm |= 1u << b;
+      }
+      sure[w][lane] = 0u;
+      cand[w][lane] = cm;
+    }
   }
-  // every block outside the neighbourhood is kept, sure, candidate, or dropped
-  int sure = 0, cand = 0;
-  if (rough) {
-#pragma unroll
-    for (int i = 0; i < chunks; ++i) {
-      const float x = score(i);
-      sure += x > top ? 1 : 0;
-      cand += (x >= bottom && x <= top) ? 1 : 0;
+  __syncwarp();
+  const bool all = take == rest;                      // (with forced blocks: every block)
+  if (choose) {
+    int n_sure = 0, n_cand = 0;
+    for (int w = 0; w < words; ++w) {
+      n_sure += __popc(sure[w][lane]);
+      n_cand += __popc(cand[w][lane]);
     }
-    sure = __reduce_add_sync(kAll, sure);
-    cand = __reduce_add_sync(kAll, cand);
-  } else if (choose) {
-    cand = rest;
-  }
-  const int want = take - sure;                       // candidates to keep
-  const bool weigh = choose && want < cand;
-  auto is_cand = [&](int i) -> bool {
-    const int j = i * 32 + lane;
-    if (rough) {
-      const float x = score(i);
-      return x >= bottom && x <= top;
-    }
-    return choose && j < nB && (j < f0 || j >= f1);
-  };
-  // 64-bit scores of the candidates in ascending order; the want-th largest
-  // key by bisection, ties to the first
-  unsigned long long pivot = 0;
-  int ties = cand;
-  if (weigh) {
-    double2 qv[E2];
+    n_sure = __reduce_add_sync(kAll, n_sure);
+    n_cand = __reduce_add_sync(kAll, n_cand);
+    const int want = take - n_sure;                   // candidates to keep
+    const bool few = n_cand <= kSelKeys;
+    if (want == n_cand) {
+      for (int w = 0; w < words; ++w) sure[w][lane] |= cand[w][lane];
+    } else {
+      // 64-bit scores of the candidates
+      double2 qv[E2];
 #pragma unroll
-    for (int u = 0; u < E2; ++u) qv[u] = *reinterpret_cast<const double2*>(mq + u * 64 + 2 * lane);
-    unsigned long long kmin = ~0ull, kmx = 0;
-    int at = 0;
+      for (int u = 0; u < E2; ++u) qv[u] = *reinterpret_cast<const double2*>(mq + u * 64 + 2 * lane);
+      int at = 0;
+#pragma unroll 1
+      for (int w = 0; w < words; ++w) {
+        const uint32_t mine = cand[w][lane];
+        for (uint32_t lanes = __ballot_sync(kAll, mine != 0u); lanes; lanes &= lanes - 1) {
+          const int src = __ffs(lanes) - 1;
+          for (uint32_t m = __shfl_sync(kAll, mine, src); m; m &= m - 1) {
+            const int b = __ffs(m) - 1;
+            const int j = 128 * (8 * w + (b >> 2)) + 4 * src + (b & 3);
+            double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < chunks; ++i) {
-      uint32_t m = __ballot_sync(kAll, is_cand(i));
-      while (m) {
-        const int j = i * 32 + __ffs(m) - 1;
-        m &= m - 1;
-        double s = 0.0;
+            for (int u = 0; u < E2; ++u) {
+              const double2 kv = *reinterpret_cast<const double2*>(mk + static_cast<size_t>(j) * D + u * 64 + 2 * lane);
+              s = fma(qv[u].x, kv.x, s);
+              s = fma(qv[u].y, kv.y, s);
+            }
 #pragma unroll
-        for (int u = 0; u < E2; ++u) {
-          const double2 kv = *reinterpret_cast<const double2*>(mk + static_cast<size_t>(j) * D + u * 64 + 2 * lane);
-          s = fma(qv[u].x, kv.x, s);
-          s = fma(qv[u].y, kv.y, s);
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+            const unsigned long long k = score_key(s);
+            if (lane == 0) {
+              if (few) {
+                s_key[warp][at] = k;
+                s_at[warp][at] = j;
+              } else {
+                __stcg(out + j, static_cast<int32_t>(k >> 32));
+                __stcg(row + j, __uint_as_float(static_cast<uint32_t>(k)));
+              }
+            }
+            ++at;
+          }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-        const unsigned long long k = score_key(s);
-        kmin = k < kmin ? k : kmin;
-        kmx = k > kmx ? k : kmx;
-        if (lane == 0) key[at] = k;
-        ++at;
+      }
+      __syncwarp();
+      auto keep_block = [&](int j) {
+        atomicOr(&sure[j >> 10][(j >> 2) & 31], 1u << (4 * ((j >> 7) & 7) + (j & 3)));
+      };
+      if (few) {
+        // a lane's candidate is kept if fewer than `want` come before it
+        const unsigned long long k = lane < n_cand ? s_key[warp][lane] : 0ull;
+        const int j = lane < n_cand ? s_at[warp][lane] : 0;
+        int before = 0;
+        for (int u = 0; u < n_cand; ++u) {
+          const unsigned long long ku = s_key[warp][u];
+          before += (ku > k || (ku == k && s_at[warp][u] < j)) ? 1 : 0;
+        }
+        if (lane < n_cand && before < want) keep_block(j);
+      } else {
+        // bisection over the 64 bits of the want-th largest key, then over the
+        // position of the last tie that is kept
+        auto key = [&](int j) -> unsigned long long {
+          return static_cast<unsigned long long>(static_cast<uint32_t>(__ldcg(out + j))) << 32 |
+                 __float_as_uint(__ldcg(row + j));
+        };
+        auto is_cand = [&](int j) -> bool {
+          return (cand[j >> 10][(j >> 2) & 31] >> (4 * ((j >> 7) & 7) + (j & 3))) & 1u;
+        };
+        unsigned long long pivot = 0;
+#pragma unroll 1
+        for (int bit = 63; bit >= 0; --bit) {
+          const unsigned long long c = pivot | (1ull << bit);
+          int n = 0;
+          for (int j = lane; j < nB; j += 32) n += is_cand(j) && key(j) >= c ? 1 : 0;
+          if (__reduce_add_sync(kAll, n) >= want) pivot = c;
+        }
+        int above = 0;
+        for (int j = lane; j < nB; j += 32) above += is_cand(j) && key(j) > pivot ? 1 : 0;
+        const int ties = want - __reduce_add_sync(kAll, above);
+        int last = nB - 1;                            // smallest j with enough ties up to it
+        for (int lo_j = 0; lo_j < last;) {
+          const int mid = (lo_j + last) / 2;
+          int n = 0;
+          for (int j = lane; j <= mid; j += 32) n += is_cand(j) && key(j) == pivot ? 1 : 0;
+          if (__reduce_add_sync(kAll, n) >= ties) last = mid;
+          else lo_j = mid + 1;
+        }
+        for (int j = lane; j < nB; j += 32) {
+          if (!is_cand(j)) continue;
+          const unsigned long long k = key(j);
+          if (k > pivot || (k == pivot && j <= last)) keep_block(j);
+        }
       }
     }
     __syncwarp();
-    pivot = kmin;
-    if (kmx != kmin) {                                // below the bits that all keys share
-      const int bits = 63 - __clzll(static_cast<long long>(kmx ^ kmin));
-      pivot = kmin >> bits >> 1 << bits << 1;
-      for (int bit = bits; bit >= 0; --bit) {
-        const unsigned long long c = pivot | (1ull << bit);
-        int n = 0;
-        for (int u = lane; u < cand; u += 32) n += key[u] >= c ? 1 : 0;
-        if (__reduce_add_sync(kAll, n) >= want) pivot = c;
+  }
+  // kept blocks in ascending order, -1 behind them
+  const uint32_t below = (1u << lane) - 1u;
+  int n = 0;
+#pragma unroll 2
+  for (int i = 0; i < used; ++i) {
+    const int j = 128 * i + 4 * lane;
+    uint32_t bits = all ? 15u : (sure[i >> 3][lane] >> (4 * (i & 7))) & 15u;
+    if (mixed(i)) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (own(j + c)) bits |= 1u << c;
+        if (j + c >= nB) bits &= ~(1u << c);
       }
     }
-    int above = 0;
-    for (int u = lane; u < cand; u += 32) above += key[u] > pivot ? 1 : 0;
-    ties = want - __reduce_add_sync(kAll, above);
-  }
-  int32_t* out = idx + (static_cast<size_t>(h) * nB + qb) * nB;
-  int n = 0, at = 0, seen = 0;
-  const uint32_t below = (1u << lane) - 1u;
+    const int own_count = __popc(bits);
+    const uint32_t b0 = __ballot_sync(kAll, own_count & 1), b1 = __ballot_sync(kAll, own_count & 2),
+                   b2 = __ballot_sync(kAll, own_count & 4);
+    int32_t* p = out + n + __popc(b0 & below) + 2 * __popc(b1 & below) + 4 * __popc(b2 & below);
 #pragma unroll
-  for (int i = 0; i < chunks; ++i) {
-    const int j = i * 32 + lane;
-    const bool in = j < nB;
-    bool kept = in && ((j >= f0 && j < f1) || (take > 0 && take == rest) || (rough && score(i) > top));
-    const bool c = is_cand(i);
-    const uint32_t cm = __ballot_sync(kAll, c);
-    if (weigh && cm) {
-      const unsigned long long k = c ? key[at + __popc(cm & below)] : 0ull;
-      const bool tie = c && k == pivot;
-      const uint32_t tm = __ballot_sync(kAll, tie);
-      kept = kept || (c && k > pivot) || (tie && seen + __popc(tm & below) < ties);
-      seen += __popc(tm);
-      at += __popc(cm);
-    } else if (c) {
-      kept = true;
-    }
-    const uint32_t km = __ballot_sync(kAll, kept);
-    if (kept) out[n + __popc(km & below)] = j;
-    n += __popc(km);
+    for (int c = 0; c < 4; ++c)
+      if (bits & (1u << c)) *p++ = j + c;
+    n += __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
   }
-  for (int j = n + lane; j < nB; j += 32) out[j] = -1;
+  if (nB % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+    const int a = min(nB, (n + 3) & ~3);
+    if (n + lane < a) out[n + lane] = -1;
+    for (int j = a + 4 * lane; j < nB; j += 128) *reinterpret_cast<int4*>(out + j) = make_int4(-1, -1, -1, -1);
+  } else {
+    for (int j = n + lane; j < nB; j += 32) out[j] = -1;
+  }
   if (lane == 0) cnt[static_cast<size_t>(h) * nB + qb] = n;
 }
 

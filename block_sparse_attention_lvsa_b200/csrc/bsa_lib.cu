@@ -800,20 +800,20 @@ bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, int es, const void* p
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMeanSelectSmem = 160 * 1024;           // keys (and long rows) of all warps of a block
-
-template <int D, int KPL>
-int launch_mean_select(const MeanWs& w, const uint8_t* ws, int H, int h0, int heads, int nB, int keep, int local,
+template <int D, int C4>
+int launch_mean_select(const MeanWs& w, uint8_t* ws, int H, int h0, int heads, int nB, int keep, int local,
                        int32_t* idx, int32_t* cnt, cudaStream_t st) {
-  static std::atomic<bool> done[kMaxDevices];
-  int rc = allow_smem(blockmean_select_kernel<D, KPL>, kMeanSelectSmem, done);
-  if (rc != BSA_OK) return rc;
-  const size_t per_warp = (static_cast<size_t>(nB) + (KPL == 0 ? (nB + 1) / 2 : 0)) * 8;
-  const int wpc = static_cast<int>(std::min<size_t>(kSelWarps, std::max<size_t>(1, kMeanSelectSmem / per_warp)));
-  const dim3 grid((nB + wpc - 1) / wpc, heads);
-  blockmean_select_kernel<D, KPL><<<grid, wpc * 32, wpc * per_warp, st>>>(
+  size_t smem = 0;
+  if (C4 == 0) {                                      // rows in shared memory
+    static std::atomic<bool> done[kMaxDevices];
+    smem = static_cast<size_t>(sel_warps(C4)) * w.ldS * 4;
+    int rc = allow_smem(blockmean_select_kernel<D, C4>, sel_warps(C4) * kMeanMaxBlocks * 4, done);
+    if (rc != BSA_OK) return rc;
+  }
+  const dim3 grid((nB + sel_warps(C4) - 1) / sel_warps(C4), heads);
+  blockmean_select_kernel<D, C4><<<grid, sel_warps(C4) * 32, smem, st>>>(
       reinterpret_cast<const double*>(ws + w.mean), reinterpret_cast<const double*>(ws + w.norm),
-      reinterpret_cast<const float*>(ws + w.scores), w.ldS, H, h0, nB, keep, local, idx, cnt);
+      reinterpret_cast<float*>(ws + w.scores), w.ldS, H, h0, nB, keep, local, idx, cnt);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -835,10 +835,11 @@ int launch_mean(const MeanWs& w, uint8_t* ws, int H, int nB, int keep, int local
     blockmean_score_kernel<D><<<dim3(tiles, tiles, hn), kScoreThreads, ScoreSmem<D>::kAlloc, st>>>(mh, ml, ms, H, h0, nB,
                                                                                               kWaitLimitNs);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    if (nB <= 256) rc = launch_mean_select<D, 8>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
-    else if (nB <= 512) rc = launch_mean_select<D, 16>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
-    else if (nB <= 1024) rc = launch_mean_select<D, 32>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
-    else if (nB <= 2048) rc = launch_mean_select<D, 64>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    if (nB <= 256) rc = launch_mean_select<D, 2>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 512) rc = launch_mean_select<D, 4>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 1024) rc = launch_mean_select<D, 8>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 1536) rc = launch_mean_select<D, 12>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
+    else if (nB <= 2048) rc = launch_mean_select<D, 16>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
     else rc = launch_mean_select<D, 0>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
     if (rc != BSA_OK) return rc;
   }

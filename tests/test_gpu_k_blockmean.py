@@ -100,6 +100,35 @@ def test_longest_rows(bsa):
         bsa.blockmean_select(big, big, 1)
 
 
+@pytest.mark.parametrize("N", [128 * 300, 128 * 700 - 5, 128 * 1537, 128 * 2048, 128 * 2100 + 1])
+def test_row_lengths(bsa, N):
+    """Rows in registers and in shared memory, with many and with few candidates
+    at the border (every second block of k is a copy of another)."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    q, k = (torch.randn((N, 1, 64), generator=g, device="cuda").bfloat16() for _ in range(2))
+    nB = -(-N // 128)
+    for copies in (False, True):
+        if copies:
+            for j in range(1, nB - 1, 2):
+                k[128 * j:128 * (j + 1)] = k[:128]
+        idx, cnt = bsa.blockmean_select(q, k, nB // 3, 1)
+        assert bsa.get_device_status() == bsa.BSA_OK
+        m = []
+        for x in (q, k):
+            p = torch.zeros((nB * 128, 64), dtype=torch.float64, device="cuda")
+            p[:N] = x[:, 0].double()
+            s = p.view(nB, 128, 64).sum(1)
+            s[-1] /= N - (nB - 1) * 128
+            s[:-1] /= 128
+            m.append(f64(s))
+        for i in sorted({0, 1, nB // 2, nB - 2, nB - 1} | set(range(0, nB, 97))):
+            # each score by itself: equal blocks get equal scores, whatever order a library adds in
+            sc = [float((m[0][i] * m[1][j]).sum()) for j in range(nB)]
+            n = int(cnt[0, i])
+            assert idx[0, i, :n].tolist() == obm.keep_row(sc, i, nB // 3, 1), (copies, i)
+            assert bool((idx[0, i, n:] == -1).all())
+
+
 def test_full_size_step(bsa):
     """One head's rows of the 6x-horizon shape among all 12 heads."""
     q, k, _ = inputs.make_qkv(196560, 12, 128, seed=10, device="cuda")
@@ -156,6 +185,10 @@ def test_stream_graph_and_own_buffers(bsa):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(idx, ref[0]) and torch.equal(cnt, ref[1])
+    room = torch.full((ref[0].numel() + 2,), -7, dtype=torch.int32, device="cuda")    # a list off the 16-byte grid
+    odd = room[1:-1].view(ref[0].shape)
+    bsa.blockmean_select(q, k, 9, 1, idx=odd)
+    assert torch.equal(odd, ref[0]) and room[0] == -7 and room[-1] == -7
     with pytest.raises(ValueError):
         bsa.blockmean_select(q, k, 9, idx=idx[:, :, :-1])
     with pytest.raises(bsa.BsaError):

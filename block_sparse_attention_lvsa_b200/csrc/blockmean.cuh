@@ -31,94 +31,165 @@
 namespace bsa {
 
 constexpr int kMeanMaxBlocks = 8192;
-constexpr int kPoolThreads = 256;
-constexpr int kPoolWarps = kPoolThreads / 32;
+constexpr int kPoolWarps = 8;                          // adding warps; one more loads
+constexpr int kPoolThreads = 32 * (kPoolWarps + 1);
+constexpr int kPoolStages = 3;                         // 32 tokens x 256 channels each
+constexpr int kPoolCtas = 3;                           // per SM
 
 // A finite bf16 times 2^-896 as a 64-bit float, by moving its bits: the sign,
 // and the exponent and significand 3 places down; the exponent then counts from
 // 1023 instead of 127, and zero and subnormals stay what they are.  `w`: the
-// bf16 in the upper half of a word.  (The conversion instruction runs at a
-// fraction of the adds' rate and held the pooling at 4.6 TB/s; with the move it
-// reads NEW TB/s.)
+// bf16 in the upper half of a word, anything in the lower.
 __device__ __forceinline__ double moved(uint32_t w) {
   return __hiloint2double(static_cast<int>((static_cast<int32_t>(w) >> 3) & 0x8FFFE000), 0);
 }
 
-// grid (nB, ceil(H * d / 256), 2): one 128-token block of 256 neighbouring
-// channels (whole heads) of q or k.  A warp reads 512 contiguous bytes per
-// token, 8 channels a lane; its 16 tokens are added in 64 bits in order, then
-// the eight warps' sums in order: bf16 values are 8 bits wide, so such a sum
-// is exact unless the block spans more than 2^38, and equal blocks always
-// give equal means.  Channels with a value that is not finite are added again
-// without the move.
+struct PoolSmem {
+  static constexpr uint32_t kStage = 32 * 512;
+  static constexpr uint32_t kSum = kPoolStages * kStage;             // [8 warps][256] double
+  static constexpr uint32_t kSq = kSum + kPoolWarps * 256 * 8;       // [8] double
+  static constexpr uint32_t kBar = kSq + kPoolWarps * 8;
+  static constexpr uint32_t kAlloc = kBar + 2 * kPoolStages * 8 + 128;
+};
+
+// Means of 128-token blocks.  A tile is one block of 256 neighbouring channels
+// (whole heads) of q or k, in four TMA boxes of 32 tokens; the blocks of the grid
+// stride over the tiles, slabs of the same tokens first.  One warp keeps
+// kPoolStages boxes in flight (with three blocks an SM 144 KB, against the 43 KB
+// that the memory's latency asks for), so that the loads do not wait for the
+// adds: with loads and adds in the same warps the pass read 4.4 TB/s, this way
+// NEW TB/s.
+//
+// The other warps add 4 tokens of each box, 8 channels a lane, in 64 bits in
+// order, then the eight warps' sums in order: bf16 values are 8 bits wide, so
+// such a sum is exact unless the block spans more than 2^38, and equal blocks
+// always give equal means.  Half of the values become 64-bit by the conversion
+// instruction, half by `moved`: each way alone holds its own pipe longer than
+// the loads take.  A channel that may hold a value that is not finite (its
+// 32-bit sum is not) is added again with the conversion.
 // mean: [2][H][nB][d] double; hi, lo: bf16 [2][H][nB][d]; norm: [2][H][nB] double.
-__global__ void __launch_bounds__(kPoolThreads) blockmean_pool_kernel(
+__global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel(
+    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
     const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, int N, int H, int d, int nB,
     double* __restrict__ mean, __nv_bfloat16* __restrict__ hi, __nv_bfloat16* __restrict__ lo,
-    double* __restrict__ norm) {
-  __shared__ double s_sum[kPoolWarps][256];
-  __shared__ double s_sq[kPoolWarps];
-  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const size_t row = static_cast<size_t>(H) * d;
-  const int c0 = blockIdx.y * 256 + lane * 8;
-  const __nv_bfloat16* x = blockIdx.z ? k : q;
-  const int rows = min(128, N - b * 128);
-  double acc[8];
+    double* __restrict__ norm, long long limit) {
+  using L = PoolSmem;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 127u) & ~127u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  double* s_sum = reinterpret_cast<double*>(gbase + L::kSum);
+  double* s_sq = reinterpret_cast<double*>(gbase + L::kSq);
+  auto full = [&](int i) -> uint32_t { return base + L::kBar + 8u * static_cast<uint32_t>(i); };
+  auto empty = [&](int i) -> uint32_t { return full(kPoolStages + i); };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = H * d, slabs = (row + 255) / 256;
+  const long long tiles = 2LL * nB * slabs;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPoolStages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), kPoolWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == kPoolWarps) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const int slab = static_cast<int>(t % slabs);
+        const int zb = static_cast<int>(t / slabs), z = zb >= nB, b = zb - z * nB;
+        for (int u = 0; u < 4; ++u, ++it) {
+          const int slot = it % kPoolStages;
+          if (it >= kPoolStages) ok = mbar_wait(empty(slot), (it / kPoolStages - 1) & 1, limit);
+          if (!ok) break;
+          mbar_arrive_expect_tx(full(slot), L::kStage);
+          tma_load_2d(base + slot * L::kStage, z ? &tmK : &tmQ, full(slot), slab * 256, b * 128 + u * 32);
+        }
+      }
+      // wait (bounded) for this thread's own copies still in flight
+      for (int u = max(0, it - kPoolStages); u < it; ++u) mbar_wait(full(u % kPoolStages), (u / kPoolStages) & 1, limit);
+    }
+    return;
+  }
+
+  int it = 0;
+  bool ok = true;
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int slab = static_cast<int>(t % slabs);
+    const int zb = static_cast<int>(t / slabs), z = zb >= nB, b = zb - z * nB;
+    const int rows = min(128, N - b * 128);
+    double acc[8];                                    // odd channels times 2^-896
+    float rough[4];                                   // 32-bit sums of the odd channels
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0;
-  if (c0 < static_cast<int>(row)) {
-    const __nv_bfloat16* p = x + (static_cast<size_t>(b) * 128 + warp * 16) * row + c0;
-    uint4 v[16];
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0;
 #pragma unroll
-    for (int t = 0; t < 16; ++t)
-      v[t] = (warp * 16 + t < rows) ? __ldg(reinterpret_cast<const uint4*>(p + t * row)) : make_uint4(0, 0, 0, 0);
-    uint32_t big[4] = {0, 0, 0, 0};                   // largest magnitude bits of each channel
+    for (int i = 0; i < 4; ++i) rough[i] = 0.f;
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u, ++it) {
+      const int slot = it % kPoolStages;
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(slot), (it / kPoolStages) & 1, limit));
+      uint4 v[4];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+      for (int i = 0; i < 4; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(gbase + slot * L::kStage + (warp * 4 + i) * 512 + lane * 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        big[i] = __vmaxu2(big[i], w[i] & 0x7FFF7FFFu);
-        acc[2 * i] += moved(w[i] << 16);
-        acc[2 * i + 1] += moved(w[i]);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[2 * c] += static_cast<double>(__uint_as_float(w[c] << 16));
+          acc[2 * c + 1] += moved(w[c]);
+          rough[c] += __uint_as_float(w[c]);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc[i] *= 0x1p+896;
-      if (((big[i / 2] >> (16 * (i & 1))) & 0xFFFFu) >= 0x7F80u) {
-        acc[i] = 0.0;
-        for (int t = 0; t < 16 && warp * 16 + t < rows; ++t)
-          acc[i] += static_cast<double>(__bfloat162float(p[t * row + i]));
+    for (int c = 0; c < 4; ++c) {
+      acc[2 * c + 1] *= 0x1p+896;
+      if (!isfinite(rough[c])) {
+        const int ch = slab * 256 + lane * 8 + 2 * c + 1;
+        const __nv_bfloat16* x = z ? k : q;
+        double s = 0.0;
+        for (int i = 0; ch < row && i < 16; ++i) {
+          const int tok = (i >> 2) * 32 + warp * 4 + (i & 3);
+          if (tok < rows) s += static_cast<double>(__bfloat162float(x[(static_cast<size_t>(b) * 128 + tok) * row + ch]));
+        }
+        acc[2 * c + 1] = s;
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_sum[warp][lane * 8 + i] = acc[i];
-  __syncthreads();
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  double m = 0.0;
-  if (c < static_cast<int>(row)) {
-#pragma unroll
-    for (int w = 0; w < kPoolWarps; ++w) m += s_sum[w][threadIdx.x];
-    m /= rows;
+    for (int i = 0; i < 8; i += 2)
+      *reinterpret_cast<double2*>(s_sum + warp * 256 + lane * 8 + i) = make_double2(acc[i], acc[i + 1]);
+    named_barrier_sync(1, kPoolWarps * 32);
+    const int c = slab * 256 + threadIdx.x;
+    double m = 0.0;
     const int h = c / d;
-    const size_t at = ((static_cast<size_t>(blockIdx.z) * H + h) * nB + b) * d + (c - h * d);
-    mean[at] = m;
-    const __nv_bfloat16 x = __float2bfloat16(static_cast<float>(m));
-    hi[at] = x;
-    lo[at] = __float2bfloat16(static_cast<float>(m - static_cast<double>(__bfloat162float(x))));
-  }
-  double sq = m * m;
+    const size_t at = ((static_cast<size_t>(z) * H + h) * nB + b) * d + (c - h * d);
+    if (c < row) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-  if (lane == 0) s_sq[warp] = sq;
-  __syncthreads();
-  const int wph = d / 32;                             // warps whose channels form one head
-  if (lane == 0 && warp % wph == 0 && c < static_cast<int>(row)) {
-    sq = 0.0;
-    for (int w = 0; w < wph; ++w) sq += s_sq[warp + w];
-    norm[(static_cast<size_t>(blockIdx.z) * H + c / d) * nB + b] = sqrt(sq);
+      for (int w = 0; w < kPoolWarps; ++w) m += s_sum[w * 256 + threadIdx.x];
+      m = rows == 128 ? m * (1.0 / 128) : m / rows;
+      mean[at] = m;
+      const __nv_bfloat16 x = __float2bfloat16(static_cast<float>(m));
+      hi[at] = x;
+      lo[at] = __float2bfloat16(static_cast<float>(m - static_cast<double>(__bfloat162float(x))));
+    }
+    double sq = m * m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+    if (lane == 0) s_sq[warp] = sq;
+    named_barrier_sync(1, kPoolWarps * 32);           // also: the sums have been read
+    const int wph = d / 32;                           // warps whose channels form one head
+    if (lane == 0 && warp % wph == 0 && c < row) {
+      sq = 0.0;
+      for (int w = 0; w < wph; ++w) sq += s_sq[warp + w];
+      norm[(static_cast<size_t>(z) * H + h) * nB + b] = sqrt(sq);
+    }
   }
 }
 

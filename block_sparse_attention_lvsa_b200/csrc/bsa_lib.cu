@@ -817,6 +817,35 @@ int launch_mean_select(const MeanWs& w, uint8_t* ws, int H, int h0, int heads, i
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+// [N, H * d] bf16 as rows, boxes of 32 tokens x 256 channels
+bool make_rows_map(CUtensorMap* m, const void* ptr, int N, int row) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(N)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row) * 2};
+  cuuint32_t box[2] = {256, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_pool(const MeanWs& w, uint8_t* ws, const void* q, const void* k, int N, int H, int d, int nB,
+                cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  int rc = allow_smem(blockmean_pool_kernel, static_cast<int>(PoolSmem::kAlloc), done);
+  if (rc != BSA_OK) return rc;
+  CUtensorMap mq, mk;
+  if (!make_rows_map(&mq, q, N, H * d) || !make_rows_map(&mk, k, N, H * d)) return BSA_ERR_CUDA;
+  const long long tiles = 2LL * nB * ((H * d + 255) / 256);
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>(tiles, 148 * kPoolCtas));
+  blockmean_pool_kernel<<<blocks, kPoolThreads, PoolSmem::kAlloc, st>>>(
+      mq, mk, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), N, H, d, nB,
+      reinterpret_cast<double*>(ws + w.mean), reinterpret_cast<__nv_bfloat16*>(ws + w.hi),
+      reinterpret_cast<__nv_bfloat16*>(ws + w.lo), reinterpret_cast<double*>(ws + w.norm), kWaitLimitNs);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 template <int D>
 int launch_mean(const MeanWs& w, uint8_t* ws, int H, int nB, int keep, int local, int32_t* idx, int32_t* cnt,
                 cudaStream_t st) {
@@ -869,13 +898,9 @@ int blockmean_select(const void* q, const void* k, int N, int H, int d, int bloc
   const int nB = n_tiles(N);
   local = std::min(local, nB);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const dim3 grid(nB, (H * d + 255) / 256, 2);
-  blockmean_pool_kernel<<<grid, kPoolThreads, 0, st>>>(
-      static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), N, H, d, nB,
-      reinterpret_cast<double*>(ws + w.mean), reinterpret_cast<__nv_bfloat16*>(ws + w.hi),
-      reinterpret_cast<__nv_bfloat16*>(ws + w.lo), reinterpret_cast<double*>(ws + w.norm));
-  if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  const int rc = d == 128 ? launch_mean<128>(w, ws, H, nB, keep, local, idx, cnt, st)
+  int rc = launch_pool(w, ws, q, k, N, H, d, nB, st);
+  if (rc != BSA_OK) return rc;
+  rc = d == 128 ? launch_mean<128>(w, ws, H, nB, keep, local, idx, cnt, st)
                           : launch_mean<64>(w, ws, H, nB, keep, local, idx, cnt, st);
   if (rc != BSA_OK) return rc;
   // the widest neighbourhood of any row

@@ -410,57 +410,67 @@ def losa_select(mass: torch.Tensor, tau: float = 0.99, idx=None, cnt=None, strea
 # ------------------------------------------- rotary positions, normed q and k ---
 _DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16, torch.float32: BSA_F32}
 _PAIRINGS = {"adjacent": BSA_ROPE_ADJACENT, "split": BSA_ROPE_SPLIT}
+_I3, _P3 = ctypes.c_int * 3, ctypes.c_void_p * 3
+_raw_stream = torch._C._cuda_getCurrentRawStream       # handle of a device's current stream, without a Stream object
 
 
-class _on_device:
-    """Makes the tensors' device current for a call and says which stream it
-    goes to; what the call allocates comes from that stream's pool, so that it
-    is not handed to other work while the call still uses it."""
-
-    def __init__(self, device: torch.device, stream):
-        self._guard = None
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self._guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _enter(device: torch.device, stream):
+    """Makes the tensors' device, and ``stream`` if given, current for a call; None where
+    they are already.  What a call allocates then comes from that stream's pool and is
+    not handed to other work while the call still uses it.  To be closed with _leave."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return None
+        guard = torch.cuda.device(device)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        guard = torch.cuda.stream(stream)
+    guard.__enter__()
+    return guard
 
 
-def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None, heads: Optional[int] = None) -> bsa_heads:
+def _leave(guard) -> None:
+    if guard is not None:
+        guard.__exit__(None, None, None)
+
+
+def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None, any_heads: bool = False) -> bsa_heads:
     """bsa_heads of a CUDA tensor [N, H, d] with unit channel stride (of the
-    type, device and sizes of ``like``; H may be given apart)."""
+    type, device and sizes of ``like``, but for H with ``any_heads``)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor of shape [N, H, d]")
-    N, H, d = t.shape
+    shape = t.shape
     if like is not None:
-        shape = (like.shape[0], like.shape[1] if heads is None else heads, like.shape[2])
-        if (N, H, d) != shape or t.dtype != like.dtype or t.device != like.device:
-            raise ValueError(f"{name} must be {like.dtype} of shape {shape} on {like.device}, "
-                             f"got {t.dtype} {(N, H, d)} on {t.device}")
+        want = like.shape
+        same = (shape[0] == want[0] and shape[2] == want[2]) if any_heads else shape == want
+        if not same or t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name} must be {like.dtype} of shape {tuple(want)} on {like.device}, "
+                             f"got {t.dtype} {tuple(shape)} on {t.device}")
     ts, hs, cs = t.stride()
-    if cs != 1 and d > 1:
+    if cs != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit channel stride")
-    return bsa_heads(t.data_ptr(), H, ts if N > 1 else 0, hs if H > 1 else 0)
+    return bsa_heads(t.data_ptr(), shape[1], ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
 
 
-def _weight(name: str, w: Optional[torch.Tensor], x: torch.Tensor) -> None:
+def _fresh(like: torch.Tensor):
+    """A new contiguous [N, H, d] tensor of ``like``'s type and device, and its bsa_heads."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    _, H, d = t.shape
+    return t, bsa_heads(t.data_ptr(), H, H * d, d)
+
+
+def _weight(name: str, w: Optional[torch.Tensor], x: torch.Tensor):
+    """The address of a norm weight [d], None without one."""
     if w is None:
-        return
+        return None
     if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, x.dtype):
         raise ValueError(f"{name} must be float32 or {x.dtype}")
-    _check_tensor(name, w, (x.shape[2],), w.dtype, x.device)
+    if w.dim() != 1 or w.shape[0] != x.shape[2] or not w.is_contiguous() or w.device != x.device:
+        raise ValueError(f"{name} must be a contiguous [{x.shape[2]}] on {x.device}")
+    return w.data_ptr()
 
 
 def _weight_type(wq, wk, x) -> int:
@@ -480,7 +490,7 @@ def _rope_for(rope: Optional[bsa_rope], x: torch.Tensor):
         raise ValueError(f"the rotation's tables are on {rope._device}, the tensor on {x.device}")
     if rope._pos is not None and rope._pos.shape[0] != x.shape[0]:
         raise ValueError(f"pos holds {rope._pos.shape[0]} tokens, the tensor {x.shape[0]}")
-    return ctypes.byref(rope)
+    return rope
 
 
 def rope_build_table(length: int, pairs: int, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
@@ -497,10 +507,13 @@ def rope_build_table(length: int, pairs: int, theta: float = 10000.0, start: flo
         raise ValueError("the table must be on a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    with _on_device(device, stream) as st:
+    guard = _enter(device, stream)
+    try:
         if table is None:
             table = torch.empty((length, pairs, 2), dtype=torch.float32, device=device)
-        rc = _lib.rope_build_table(length, pairs, float(theta), float(start), float(step), _ptr(table), st)
+        rc = _lib.rope_build_table(length, pairs, theta, start, step, table.data_ptr(), _raw_stream(device.index))
+    finally:
+        _leave(guard)
     _check("rope_build_table", rc)
     return table
 
@@ -515,34 +528,37 @@ def rope_axes(tables, grid=None, first=(0, 0, 0), pos: Optional[torch.Tensor] = 
     not turned), or ``pos`` (int32 [N, 3]) lists the positions (negative: not
     turned along that axis).  ``pairing``: "adjacent" channels 2j, 2j+1 or
     "split" channels j, j+d/2 form a pair."""
-    tables = list(tables)
-    if not 1 <= len(tables) <= 3:
+    n = len(tables)
+    if not 1 <= n <= 3:
         raise ValueError("rope_axes takes one to three tables")
     if pairing not in _PAIRINGS:
         raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}")
     if (grid is None) == (pos is None):
         raise ValueError("give either grid or pos")
-    r = bsa_rope()
-    r.pairing = _PAIRINGS[pairing]
     dev = None
+    pairs, lens, ptrs = [0, 0, 0], [0, 0, 0], [None, None, None]
     for a, t in enumerate(tables):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_cuda:
-            raise ValueError("a table must be a float32 CUDA tensor [len, pairs, 2]")
-        dev = t.device if dev is None else dev
-        _check_tensor("table", t, (t.shape[0], t.shape[1], 2), torch.float32, dev)
-        r.pairs[a], r.len[a], r.table[a] = t.shape[1], t.shape[0], t.data_ptr()
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 3 or not t.is_cuda or \
+                t.shape[2] != 2 or not t.is_contiguous():
+            raise ValueError("a table must be a contiguous float32 CUDA tensor [len, pairs, 2]")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"the tables are on {dev} and {t.device}")
+        lens[a], pairs[a], _ = t.shape
+        ptrs[a] = t.data_ptr()
+    g, f = (1, 1, 1), (0, 0, 0)
     if pos is not None:
         _check_tensor("pos", pos, (pos.shape[0], 3), torch.int32, dev)
-        r.pos = pos.data_ptr()
     else:
         grid, first = tuple(grid), tuple(first)
-        if len(grid) != len(tables) or len(first) < len(grid):
+        if len(grid) != n or len(first) < n:
             raise ValueError("grid and first must give every axis")
-        for a in range(3):
-            r.grid[a] = grid[a] if a < len(grid) else 1
-            r.first[a] = first[a] if a < len(grid) else 0
+        g, f = grid + (1,) * (3 - n), first[:n] + (0,) * (3 - n)
+    r = bsa_rope(_PAIRINGS[pairing], _I3(*pairs), _I3(*lens), _P3(*ptrs), _I3(*g), _I3(*f),
+                 None if pos is None else pos.data_ptr())
     r._device, r._pos = dev, pos
-    r._tensors = (tables, pos)             # the struct holds raw pointers: keep the tensors alive with it
+    r._tensors = (tuple(tables), pos)      # the struct holds raw pointers: keep the tensors alive with it
     return r
 
 
@@ -551,15 +567,19 @@ def rope_apply(x: torch.Tensor, rope: bsa_rope, inverse: bool = False, out: Opti
     """x [N, H, d] turned by its tokens' positions (``inverse``: turned back, which is
     also the gradient).  ``out`` may be x itself; x may be a strided slice."""
     hx = _heads("x", x)
-    rp = _rope_for(rope, x)
-    if rp is None:
+    if _rope_for(rope, x) is None:
         raise ValueError("rope must come from rope_axes")
-    N, H, d = x.shape
-    with _on_device(x.device, stream) as st:
+    dev = x.device
+    guard = _enter(dev, stream)
+    try:
         if out is None:
-            out = torch.empty((N, H, d), dtype=x.dtype, device=x.device)
-        rc = _lib.rope_apply(ctypes.byref(hx), ctypes.byref(_heads("out", out, x)), _DTYPES[x.dtype], N, d, rp,
-                             int(bool(inverse)), st)
+            out, ho = _fresh(x)
+        else:
+            ho = _heads("out", out, x)
+        rc = _lib.rope_apply(hx, ho, _DTYPES[x.dtype], x.shape[0], x.shape[2], rope, bool(inverse),
+                             _raw_stream(dev.index))
+    finally:
+        _leave(guard)
     _check("rope_apply", rc)
     return out
 
@@ -571,24 +591,29 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], wq: Optional[to
     None), then the rotation (None: none), in one pass; returns (qo, ko).  k may be
     None (then ko is).  An output may be its own input."""
     hq = _heads("q", q)
-    hk = None if k is None else _heads("k", k, q, k.shape[1] if k.dim() == 3 else None)
     if k is None and (wk is not None or ko is not None):
         raise ValueError("wk and ko need k")
-    _weight("wq", wq, q)
-    _weight("wk", wk, q)
+    hk = None if k is None else _heads("k", k, q, True)
+    pq, pk = _weight("wq", wq, q), _weight("wk", wk, q)
     wtype = _weight_type(wq, wk, q)
-    rp = _rope_for(rope, q)
-    N, _, d = q.shape
-    with _on_device(q.device, stream) as st:
+    rope = _rope_for(rope, q)
+    dev = q.device
+    guard = _enter(dev, stream)
+    try:
         if qo is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if ko is None and k is not None:
-            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        ho = _heads("qo", qo, q)
-        hko = None if k is None else _heads("ko", ko, k)
-        rc = _lib.qk_norm_rope_fwd(ctypes.byref(hq), None if k is None else ctypes.byref(hk), ctypes.byref(ho),
-                                   None if k is None else ctypes.byref(hko), _DTYPES[q.dtype], N, d, _ptr(wq),
-                                   _ptr(wk), wtype, float(eps), rp, st)
+            qo, hqo = _fresh(q)
+        else:
+            hqo = _heads("qo", qo, q)
+        hko = None
+        if k is not None:
+            if ko is None:
+                ko, hko = _fresh(k)
+            else:
+                hko = _heads("ko", ko, k)
+        rc = _lib.qk_norm_rope_fwd(hq, hk, hqo, hko, _DTYPES[q.dtype], q.shape[0], q.shape[2], pq, pk, wtype, eps,
+                                   rope, _raw_stream(dev.index))
+    finally:
+        _leave(guard)
     _check("qk_norm_rope_fwd", rc)
     return qo, ko
 
@@ -603,32 +628,40 @@ def qk_norm_rope_bwd(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tens
     hgq = _heads("gq", gq, q)
     if (gk is None) != (k is None) or (k is None and (wk is not None or dk is not None)):
         raise ValueError("gk, wk and dk need k, and k needs gk")
-    hk = None if k is None else _heads("k", k, q, k.shape[1] if k.dim() == 3 else None)
-    hgk = None if k is None else _heads("gk", gk, k)
-    _weight("wq", wq, q)
-    _weight("wk", wk, q)
+    hk = hgk = None
+    if k is not None:
+        hk, hgk = _heads("k", k, q, True), _heads("gk", gk, k)
+    pq, pk = _weight("wq", wq, q), _weight("wk", wk, q)
     wtype = _weight_type(wq, wk, q)
-    rp = _rope_for(rope, q)
-    _check_workspace(workspace, q.device)
+    rope = _rope_for(rope, q)
+    dev = q.device
+    _check_workspace(workspace, dev)
     N, H, d = q.shape
-    need = int(_lib.qk_norm_rope_bwd_workspace_bytes(N, H, 0 if k is None else k.shape[1], d))
+    need = _lib.qk_norm_rope_bwd_workspace_bytes(N, H, 0 if k is None else k.shape[1], d)
     if need == ctypes.c_size_t(-1).value:
-        raise BsaError("qk_norm_rope_bwd_workspace_bytes", BSA_ERR_ARG)
-    with _on_device(q.device, stream) as st:
+        raise BsaError("qk_norm_rope_bwd_workspace_bytes", BSA_ERR_UNSUPPORTED)
+    guard = _enter(dev, stream)
+    try:
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if dk is None and k is not None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            dq, hdq = _fresh(q)
+        else:
+            hdq = _heads("dq", dq, q)
+        hdk = None
+        if k is not None:
+            if dk is None:
+                dk, hdk = _fresh(k)
+            else:
+                hdk = _heads("dk", dk, k)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        dwq = None if wq is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        dwk = None if wk is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        hdq = _heads("dq", dq, q)
-        hdk = None if k is None else _heads("dk", dk, k)
-        opt = lambda h: None if h is None else ctypes.byref(h)      # noqa: E731
-        rc = _lib.qk_norm_rope_bwd(opt(hgq), opt(hgk), opt(hq), opt(hk), opt(hdq), opt(hdk), _DTYPES[q.dtype], N, d,
-                                   _ptr(wq), _ptr(wk), wtype, float(eps), rp, _ptr(dwq), _ptr(dwk), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), st)
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        dwq = None if wq is None else torch.empty_like(wq, dtype=torch.float32)
+        dwk = None if wk is None else torch.empty_like(wk, dtype=torch.float32)
+        rc = _lib.qk_norm_rope_bwd(hgq, hgk, hq, hk, hdq, hdk, _DTYPES[q.dtype], N, d, pq, pk, wtype, eps, rope,
+                                   None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _raw_stream(dev.index))
+    finally:
+        _leave(guard)
     _check("qk_norm_rope_bwd", rc)
     return dq, dk, dwq, dwk
 
@@ -647,18 +680,23 @@ def blockmean_select(q: torch.Tensor, k: torch.Tensor, keep: int, local: int = 0
     nB = math.ceil(N / 128)
     _check_tensor("idx", idx, (H, nB, nB), torch.int32, q.device)
     _check_tensor("cnt", cnt, (H, nB), torch.int32, q.device)
-    need = int(_lib.blockmean_select_workspace_bytes(N, H, d))
+    need = _lib.blockmean_select_workspace_bytes(N, H, d)
     if need == ctypes.c_size_t(-1).value:
         raise BsaError("blockmean_select", BSA_ERR_UNSUPPORTED)
-    with _on_device(q.device, stream) as st:
+    dev = q.device
+    guard = _enter(dev, stream)
+    try:
         if idx is None:
-            idx = torch.empty((H, nB, nB), dtype=torch.int32, device=q.device)
+            idx = q.new_empty((H, nB, nB), dtype=torch.int32)
         if cnt is None:
-            cnt = torch.empty((H, nB), dtype=torch.int32, device=q.device)
+            cnt = q.new_empty((H, nB), dtype=torch.int32)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        rc = _lib.blockmean_select(_ptr(q), _ptr(k), N, H, d, int(block), int(keep), int(local), _ptr(idx), _ptr(cnt),
-                                   _ptr(workspace), workspace.numel() * workspace.element_size(), st)
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        rc = _lib.blockmean_select(q.data_ptr(), k.data_ptr(), N, H, d, int(block), int(keep), int(local),
+                                   idx.data_ptr(), cnt.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
+    finally:
+        _leave(guard)
     _check("blockmean_select", rc, (BSA_OK, BSA_WARN_OVER_BUDGET))
     return idx, cnt
 
@@ -688,13 +726,17 @@ def blocksparse_attn_bwd(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     if scale is None:
         scale = d ** -0.5
     need = workspace_bytes(BSA_OP_BLOCKSPARSE_BWD, N, H, d, index)
-    with _on_device(dev, stream) as st:
+    guard = _enter(dev, stream)
+    try:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(need, dtype=torch.uint8)
         dq, dk, dv = (torch.empty_like(q) if t is None else t for t in (dq, dk, dv))
-        rc = _lib.blocksparse_attn_bwd(_ptr(go), _ptr(q), _ptr(k), _ptr(v), ctypes.byref(ho), _ptr(lse), N, H, d, float(scale),
-                                       ctypes.byref(index), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), st)
+        rc = _lib.blocksparse_attn_bwd(go.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), ho, lse.data_ptr(),
+                                       N, H, d, scale, index, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       _raw_stream(dev.index))
+    finally:
+        _leave(guard)
     _check("blocksparse_attn_bwd", rc)
     return dq, dk, dv
 

@@ -15,22 +15,28 @@
 //   attn_bwd_dkv_kernel  one CTA per 128-key tile and head, over the query
 //     tiles that list it (the index transposed on the device).  Tiles are
 //     held transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and dS^T
-//     (bf16, written over them in TMEM) are the A operands of
-//     dV += P^T dO and dK += dS^T Q and never touch shared memory.
+//     (bf16, in TMEM) are the A operands of dV += P^T dO and dK += dS^T Q and
+//     never touch shared memory.  TMEM is full (S, dP, dV, dK, 128 columns
+//     each at d = 128): P and dS both lie over dP, so that S is free again as
+//     soon as its scores are in registers and the next tile's S runs during
+//     the exponentials.
 //   attn_bwd_dq_kernel   one CTA per 128-query tile and head, over its own
 //     list: S = Q K^T, dP = dO V^T, dQ += dS K.
 //
-// Warp roles (384 threads), as in the forward:
-//   warp 0        TMA producer          warp 1   tcgen05.mma issuer
-//   warps 4..7    columns 0..63 of every tile (thread = TMEM lane = row)
-//   warps 8..11   columns 64..127
-// A thread turns 64 scores into probabilities (kept in registers in 32 bits
-// for ds) while the tensor core runs the products of the neighbouring steps:
-//   dkv:  dV(i), S(i+1) | dK(i), dP(i+1)       dq:  dP(j+1), dQ(j), S(j+2)
+// Warp roles (640 threads):
+//   warp 0         TMA producer          warp 1   tcgen05.mma issuer
+//   warps 4..19    four groups of 4 warps; group g turns columns
+//                  32 g .. 32 g + 31 of every tile, thread = TMEM lane = row
+// What a thread does with a tile (read S, 32 exponentials, read dP, form ds,
+// write P and dS) is a chain of latencies; with two groups of 64 columns it
+// took ~3,300 cycles a tile against 2,048 of tensor work (clock trace), with
+// four groups the chains are half as long and twice as many overlap.
+// setmaxnreg gives the groups 104 registers a thread and the other warps 56.
+//   tensor order, dkv:  S(i+1), dV(i), dK(i), dP(i+1)
+//                 dq:   dP(j+1), dQ(j), S(j+2)
 // P and dS are rounded to bf16 for the products (half a step, at most 2^-8
-// of each term, as P is in the forward); all sums are 32-bit.  Each half of the
-// columns is written over its own half of the scores, so the two warpgroups
-// never wait for one another.
+// of each term, as P is in the forward); all sums are 32-bit.  Each group
+// writes over its own columns, so the groups never wait for one another.
 #pragma once
 #include "attn_fwd.cuh"
 
@@ -60,15 +66,34 @@ struct BwdParams {
   long long wait_limit_ns;
 };
 
-constexpr int kBwdThreads = 384;
+constexpr int kBwdGroups = 4;                      // of 128 threads
+constexpr int kBwdCols = 128 / kBwdGroups;         // columns of a tile per group
+constexpr int kBwdThreads = 128 + 128 * kBwdGroups;
+// launched with at most 96 registers a thread (640 x 96 = 61,440)
+constexpr int kBwdRegsLow = 56, kBwdRegsHigh = 104;
+static_assert(kBwdRegsLow * 128 + kBwdRegsHigh * 128 * kBwdGroups <= 96 * kBwdThreads, "register split");
 constexpr int kPartialBit = 1 << 30;
 
-// 64 consecutive columns of the thread's TMEM lane, complete on return
-__device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-               "tcgen05.wait::ld.sync.aligned;"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-               : "r"(taddr) : "memory");
+// D[tmem] (+)= A[tmem] * B[smem] for two consecutive K-steps of 16 (see
+// mma4_ts_warp).
+__device__ __forceinline__ void mma2_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate_first) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1;\n\t.reg .b32 a1;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 t, %5, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate_first), "r"(1u)
+      : "memory");
+}
+// 16 columns written and complete on return
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+               "tcgen05.wait::st.sync.aligned;"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
@@ -194,42 +219,36 @@ __global__ void __launch_bounds__(128) attn_bwd_lists_kernel(int nB, const uint3
   if (kt < nB) tcount[static_cast<size_t>(h) * nB + kt] = n;
 }
 
-__device__ __forceinline__ void set_bits64(uint32_t (&mw)[2], int a, int b) {
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int lo = max(a, 32 * w), hi = min(b, 32 * w + 32);
-    if (lo < hi) mw[w] |= (hi - lo == 32 ? 0xFFFFFFFFu : ((1u << (hi - lo)) - 1u)) << (lo - 32 * w);
-  }
+__device__ __forceinline__ uint32_t bits32(int a, int b) {          // bits a .. b - 1, 0 <= a < b <= 32
+  return (b - a == 32 ? 0xFFFFFFFFu : (1u << (b - a)) - 1u) << a;
 }
 __device__ __forceinline__ bool frame_bit(const BwdParams& p, int fq, int fk) {
   return (__ldg(p.fbits + static_cast<size_t>(fq) * p.TW + (fk >> 5)) >> (fk & 31)) & 1u;
 }
-// Element mask of 64 query columns for key frame fk: bit c set iff query q0+c
+// Element mask of 32 query columns for key frame fk: bit c set iff query q0+c
 // < N may attend it.
-__device__ __forceinline__ void query_mask(const BwdParams& p, int fk, int q0, uint32_t (&mw)[2]) {
-  mw[0] = mw[1] = 0u;
-  const int qend = min(q0 + 64, p.N);
+__device__ __forceinline__ uint32_t query_mask(const BwdParams& p, int fk, int q0) {
+  uint32_t m = 0u;
+  const int qend = min(q0 + kBwdCols, p.N);
   for (int f = q0 / p.P; f * p.P < qend; ++f)
-    if (frame_bit(p, f, fk)) set_bits64(mw, max(f * p.P, q0) - q0, min((f + 1) * p.P, qend) - q0);
+    if (frame_bit(p, f, fk)) m |= bits32(max(f * p.P, q0) - q0, min((f + 1) * p.P, qend) - q0);
+  return m;
 }
-// Element mask of 64 key columns for query frame fq (no frames: every key < N).
-__device__ __forceinline__ void key_mask(const BwdParams& p, int fq, int k0, uint32_t (&mw)[2]) {
-  mw[0] = mw[1] = 0u;
-  const int kend = min(k0 + 64, p.N);
-  if (p.fbits == nullptr) {
-    set_bits64(mw, 0, kend - k0);
-    return;
-  }
+// Element mask of 32 key columns for query frame fq (no frames: every key < N).
+__device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0) {
+  uint32_t m = 0u;
+  const int kend = min(k0 + kBwdCols, p.N);
+  if (p.fbits == nullptr) return k0 < kend ? bits32(0, kend - k0) : 0u;
   for (int f = k0 / p.P; f * p.P < kend; ++f)
-    if (frame_bit(p, fq, f)) set_bits64(mw, max(f * p.P, k0) - k0, min((f + 1) * p.P, kend) - k0);
+    if (frame_bit(p, fq, f)) m |= bits32(max(f * p.P, k0) - k0, min((f + 1) * p.P, kend) - k0);
+  return m;
 }
 
-// One row of an f32 accumulator (TMEM) to bf16 in a 128-byte-swizzled tile in
-// shared memory, times `mul`; zeros when !have.
-template <int D>
-__device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sTile, int r, float mul, bool have) {
+// 64 columns of one row of an f32 accumulator (TMEM) to bf16 in a
+// 128-byte-swizzled box in shared memory, times `mul`; zeros when !have.
+__device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sBox, int r, float mul, bool have) {
 #pragma unroll
-  for (int c0 = 0; c0 < D; c0 += 32) {
+  for (int c0 = 0; c0 < 64; c0 += 32) {
     uint32_t ov[32];
     __syncwarp();
     if (have) {
@@ -240,8 +259,7 @@ __device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sTile, int r,
     }
 #pragma unroll
     for (int v4 = 0; v4 < 4; ++v4) {
-      const int col = c0 + 8 * v4;
-      const uint32_t dst = sTile + (col / 64) * (128 * 128) + r * 128 + ((((col % 64) / 8) ^ (r & 7)) * 16);
+      const uint32_t dst = sBox + r * 128 + (((c0 / 8 + v4) ^ (r & 7)) * 16);
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -255,18 +273,27 @@ template <int D>
 struct BwdSmem {
   static constexpr uint32_t kBox = 128 * 128;
   static constexpr uint32_t kTile = (D / 64) * kBox;
-  // dkv: K, V, then two stages of Q, dO, and of nl, nd (128 floats each)
-  // dq:  Q, dO, then three K and two V tiles
-  static constexpr uint32_t kA = 0, kB = kTile, kRing = 2 * kTile;
-  static constexpr uint32_t kBar = kRing + 5 * kTile;
+  // dkv: K, V, three Q and two dO tiles, nl and nd beside each dO (128 floats
+  // each); dq: Q, dO, three K and two V tiles
+  static constexpr uint32_t kA = 0, kB = kTile, kRing3 = 2 * kTile, kRing2 = 5 * kTile;
+  static constexpr uint32_t kRows = 7 * kTile;
+  static constexpr uint32_t kBar = kRows + 2 * 1024;
   static constexpr uint32_t kHolder = kBar + 32 * 8;
-  static constexpr uint32_t kAlloc = kHolder + 16 + 1024;           // + alignment slack
+  // declared 1,024-byte aligned: at d = 128 there is no room for slack
+  static constexpr uint32_t kAlloc = kHolder + 16;
 };
-// dkv keeps nl and nd in the fifth ring tile
-template <int D>
-constexpr uint32_t kDkvRows = BwdSmem<D>::kRing + 4 * BwdSmem<D>::kTile;
+static_assert(BwdSmem<128>::kAlloc <= 232448, "shared memory of one block");
 
-enum : int { W_AB = 0, W_QFULL = 1, W_OFULL = 3, W_QEMPTY = 5, W_OEMPTY = 7, W_SFULL = 9, W_DPFULL = 10, W_P = 11, W_DS = 13, W_FINAL = 15 };
+enum : int {
+  W_AB = 0,                           // K and V loaded
+  W_QFULL = 1, W_QEMPTY = 4,          // [3]
+  W_OFULL = 7, W_OEMPTY = 9,          // [2] dO, nl, nd
+  W_SFULL = 11, W_SFREE = 12, W_DPFULL = 13,
+  W_P = 14, W_DS = W_P + kBwdGroups,  // [group]
+  W_FINAL = W_DS + kBwdGroups,
+  W_COUNT
+};
+static_assert(W_COUNT <= 32, "barrier slots");
 
 // dK and dV of one key tile.
 template <int D>
@@ -276,12 +303,15 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                     const BwdParams p) {
   using L = BwdSmem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_bwd[];
+  const uint32_t base = smem_u32(smem_bwd);
+  if (base & 1023u) {                                   // the swizzled tiles need the declared alignment
+    set_status(BSA_ERR_CUDA);
+    return;
+  }
   const uint32_t bar0 = base + L::kBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + L::kHolder);
+  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_bwd + L::kHolder);
 
   const int kt = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -291,7 +321,8 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int NP = p.nB * 128;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 16; ++i) mbar_init(bar(i), (i >= W_P && i < W_FINAL) ? 4 : 1);
+    for (int i = 0; i < W_COUNT; ++i)
+      mbar_init(bar(i), i == W_SFREE ? 4 * kBwdGroups : ((i >= W_P && i < W_FINAL) ? 4 : 1));
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -305,11 +336,12 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 256, kTDK = 256 + D;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescD = idesc_bf16_f32(128, D, false, true);
-  auto sQ = [&](int i) -> uint32_t { return base + L::kRing + (i & 1) * 2 * L::kTile; };
-  auto sG = [&](int i) -> uint32_t { return base + L::kRing + ((i & 1) * 2 + 1) * L::kTile; };
-  auto sRow = [&](int i) -> uint32_t { return base + kDkvRows<D> + (i & 1) * 1024; };
+  auto sQ = [&](int i) -> uint32_t { return base + L::kRing3 + (i % 3) * L::kTile; };
+  auto sG = [&](int i) -> uint32_t { return base + L::kRing2 + (i & 1) * L::kTile; };
+  auto sRow = [&](int i) -> uint32_t { return base + L::kRows + (i & 1) * 1024; };
 
   if (warp == 0) {
+    regs_dec<kBwdRegsLow>();
     if (lane == 0 && n > 0) {
       mbar_arrive_expect_tx(bar(W_AB), 2 * L::kTile);
 #pragma unroll
@@ -321,19 +353,19 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       bool ok = true;
       for (int i = 0; i < n; ++i) {
         const int qt = lst[i] & ~kPartialBit;
-        if (i >= 2) ok = mbar_wait(bar(W_QEMPTY + (i & 1)), ((i >> 1) - 1) & 1, limit);
+        if (i >= 3) ok = mbar_wait(bar(W_QEMPTY + i % 3), (i / 3 - 1) & 1, limit);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(W_QFULL + (i & 1)), L::kTile + 1024);
+        mbar_arrive_expect_tx(bar(W_QFULL + i % 3), L::kTile);
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(sQ(i) + b * L::kBox, &tmQ, bar(W_QFULL + (i & 1)), b * 64, h, qt * 128);
-        const size_t at = static_cast<size_t>(h) * NP + static_cast<size_t>(qt) * 128;
-        bulk_load(sRow(i), p.nl + at, 512, bar(W_QFULL + (i & 1)));
-        bulk_load(sRow(i) + 512, p.nd + at, 512, bar(W_QFULL + (i & 1)));
+          tma_load_3d(sQ(i) + b * L::kBox, &tmQ, bar(W_QFULL + i % 3), b * 64, h, qt * 128);
         ++nq;
         if (i >= 2) ok = mbar_wait(bar(W_OEMPTY + (i & 1)), ((i >> 1) - 1) & 1, limit);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(W_OFULL + (i & 1)), L::kTile);
+        mbar_arrive_expect_tx(bar(W_OFULL + (i & 1)), L::kTile + 1024);
+        const size_t at = static_cast<size_t>(h) * NP + static_cast<size_t>(qt) * 128;
+        bulk_load(sRow(i), p.nl + at, 512, bar(W_OFULL + (i & 1)));
+        bulk_load(sRow(i) + 512, p.nd + at, 512, bar(W_OFULL + (i & 1)));
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
           tma_load_3d(sG(i) + b * L::kBox, &tmG, bar(W_OFULL + (i & 1)), b * 64, h, qt * 128);
@@ -341,10 +373,11 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
       // drain: wait (bounded) for this thread's own copies still in flight
       mbar_wait(bar(W_AB), 0, limit);
-      for (int u = max(0, nq - 2); u < nq; ++u) mbar_wait(bar(W_QFULL + (u & 1)), (u >> 1) & 1, limit);
+      for (int u = max(0, nq - 3); u < nq; ++u) mbar_wait(bar(W_QFULL + u % 3), (u / 3) & 1, limit);
       for (int u = max(0, no - 2); u < no; ++u) mbar_wait(bar(W_OFULL + (u & 1)), (u >> 1) & 1, limit);
     }
   } else if (warp == 1) {
+    regs_dec<kBwdRegsLow>();
     if (n > 0) {
       const uint64_t dK = desc64(sw128_desc(base + L::kA, 16, 1024)), dV = desc64(sw128_desc(base + L::kB, 16, 1024));
       // S^T = K Q_i^T
@@ -363,6 +396,18 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           mma4_ss_warp(tbase + kTDP, dV + g * (L::kBox >> 4), dg + g * (L::kBox >> 4), kIdescS, g > 0);
         tc_commit_warp(bar(W_DPFULL));
       };
+      // dst += A^T B, 32 queries of A (in dP's columns from `off`) as each group stores them
+      auto grad_mma = [&](uint32_t dst, uint32_t off, uint32_t tile, int first_bar, int i) -> bool {
+        const uint64_t db = desc64(sw128_desc(tile, L::kBox, 1024));
+#pragma unroll
+        for (int g = 0; g < kBwdGroups; ++g) {
+          if (!mbar_wait_warp(bar(first_bar + g), i & 1, limit)) return false;
+          tc_fence_after();
+          mma2_ts_warp(tbase + dst, tbase + kTDP + off + g * kBwdCols, db + g * (kBwdCols * 128 >> 4), kIdescD,
+                       (i > 0 || g > 0) ? 1u : 0u);
+        }
+        return true;
+      };
       bool ok = mbar_wait_warp(bar(W_AB), 0, limit) && mbar_wait_warp(bar(W_QFULL), 0, limit);
       tc_fence_after();
       if (ok) s_mma(0);
@@ -371,43 +416,31 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       if (ok) dp_mma(0);
       for (int i = 0; ok && i < n; ++i) {
         const int nx = i + 1;
-        // dV += P^T dO_i, 64 queries at a time
-        const uint64_t dg = desc64(sw128_desc(sG(i), L::kBox, 1024));
-        if (!(ok = mbar_wait_warp(bar(W_P), i & 1, limit))) break;
-        tc_fence_after();
-        mma4_ts_warp(tbase + kTDV, tbase + kTS, dg, kIdescD, i > 0);
-        if (!(ok = mbar_wait_warp(bar(W_P + 1), i & 1, limit))) break;
-        tc_fence_after();
-        mma4_ts_warp(tbase + kTDV, tbase + kTS + 64, dg + 512, kIdescD, 1u);
-        tc_commit_warp(bar(W_OEMPTY + (i & 1)));
+        // S of the next tile as soon as this one's scores are in registers
         if (nx < n) {
-          if (!(ok = mbar_wait_warp(bar(W_QFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+          if (!(ok = mbar_wait_warp(bar(W_QFULL + nx % 3), (nx / 3) & 1, limit))) break;
+          if (!(ok = mbar_wait_warp(bar(W_SFREE), i & 1, limit))) break;
           tc_fence_after();
           s_mma(nx);
         }
-        // dK += dS^T Q_i
-        const uint64_t dq = desc64(sw128_desc(sQ(i), L::kBox, 1024));
-        if (!(ok = mbar_wait_warp(bar(W_DS), i & 1, limit))) break;
-        tc_fence_after();
-        mma4_ts_warp(tbase + kTDK, tbase + kTDP, dq, kIdescD, i > 0);
-        if (!(ok = mbar_wait_warp(bar(W_DS + 1), i & 1, limit))) break;
-        tc_fence_after();
-        mma4_ts_warp(tbase + kTDK, tbase + kTDP + 64, dq + 512, kIdescD, 1u);
-        tc_commit_warp(bar(W_QEMPTY + (i & 1)));
-        if (nx < n) {
-          if (!(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
-          tc_fence_after();
-          dp_mma(nx);
-        }
+        if (!(ok = grad_mma(kTDV, 0, sG(i), W_P, i))) break;                       // dV += P^T dO_i
+        tc_commit_warp(bar(W_OEMPTY + (i & 1)));
+        if (nx < n && !(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+        if (!(ok = grad_mma(kTDK, kBwdCols / 2, sQ(i), W_DS, i))) break;           // dK += dS^T Q_i
+        tc_commit_warp(bar(W_QEMPTY + i % 3));
+        if (nx < n) dp_mma(nx);
       }
       tc_commit_warp(bar(W_FINAL));
       mbar_wait_warp(bar(W_FINAL), 0, limit);
     }
-  } else if (warp >= 4) {
-    const int g = (warp - 4) >> 2;                      // columns 64 g .. 64 g + 63
+  } else if (warp < 4) {
+    regs_dec<kBwdRegsLow>();
+  } else {
+    regs_inc<kBwdRegsHigh>();
+    const int g = (warp - 4) >> 2;
     const int r = (threadIdx.x - 128) & 127;
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tS = tbase + lane_off + kTS + 64 * g, tDP = tbase + lane_off + kTDP + 64 * g;
+    const uint32_t tS = tbase + lane_off + kTS + kBwdCols * g, tDP = tbase + lane_off + kTDP + kBwdCols * g;
     const int fk = p.fbits != nullptr ? min(kt * 128 + r, p.N - 1) / p.P : 0;
     const uint64_t sl2p = f2pack(p.sl2, p.sl2);
     bool ok = true;
@@ -416,19 +449,22 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const int e = e_next;
       if (i + 1 < n) e_next = ld_pinned_s32(lst + i + 1);
       const bool part = (e & kPartialBit) != 0 && p.fbits != nullptr;
-      uint32_t mw[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-      if (part) query_mask(p, fk, (e & ~kPartialBit) * 128 + 64 * g, mw);
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_QFULL + (i & 1)), (i >> 1) & 1, limit) &&
-                                       mbar_wait(bar(W_SFULL), i & 1, limit));
+      uint32_t mw = 0xFFFFFFFFu;
+      if (part) mw = query_mask(p, fk, (e & ~kPartialBit) * 128 + kBwdCols * g);
+      ok = mbar_wait(bar(W_OFULL + (i & 1)), (i >> 1) & 1, limit);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_SFULL), i & 1, limit) && ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t rowv = sRow(i) + 256 * g;
-      uint32_t sr[64];
+      const uint32_t rowv = sRow(i) + 4 * kBwdCols * g;
+      uint32_t sr[32];
       float* pv = reinterpret_cast<float*>(sr);
-      tmem_ld_x64(tS, sr);
-      uint32_t pk[32];
+      tmem_ld_x32(tS, sr);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(W_SFREE));
+      uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
+      for (int c = 0; c < kBwdCols; c += 4) {
         const float4 nl = ld_shared_f4(rowv + 4 * c);
         const uint64_t x01 = ffma2(f2pack(pv[c], pv[c + 1]), sl2p, f2pack(nl.x, nl.y));
         const uint64_t x23 = ffma2(f2pack(pv[c + 2], pv[c + 3]), sl2p, f2pack(nl.z, nl.w));
@@ -439,57 +475,62 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         pv[c + 1] = ex2_approx(x1);
         pv[c + 2] = ex2_approx(x2);
         pv[c + 3] = ex2_approx(x3);
-        if (part) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (!((mw[(c + u) >> 5] >> ((c + u) & 31)) & 1u)) pv[c + u] = 0.f;
-        }
-        pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
-        pk[c / 2 + 1] = pack_bf16x2(pv[c + 2], pv[c + 3]);
       }
-      tmem_st_x32(tS, pk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(W_P + g));
+      if (part) {
+#pragma unroll
+        for (int c = 0; c < kBwdCols; ++c)
+          if (!((mw >> c) & 1u)) pv[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < kBwdCols; c += 2) pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_DPFULL), i & 1, limit));
       if (!ok) break;
       tc_fence_after();
-      uint32_t dr[64];
-      const float* dv = reinterpret_cast<const float*>(dr);
-      tmem_ld_x64(tDP, dr);
+      // dP of these columns goes to registers, P takes the first half of them,
+      // dS the second; nd is read before P is signalled, which lets go of the rows
+      uint32_t dr[32];
+      float* dv = reinterpret_cast<float*>(dr);
+      tmem_ld_x32(tDP, dr);
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
+      for (int c = 0; c < kBwdCols; c += 4) {
         const float4 nd = ld_shared_f4(rowv + 512 + 4 * c);
-        const uint64_t y01 = fmul2(f2pack(pv[c], pv[c + 1]), fadd2(f2pack(dv[c], dv[c + 1]), f2pack(nd.x, nd.y)));
-        const uint64_t y23 =
-            fmul2(f2pack(pv[c + 2], pv[c + 3]), fadd2(f2pack(dv[c + 2], dv[c + 3]), f2pack(nd.z, nd.w)));
-        float y0, y1, y2, y3;
-        f2unpack(y01, y0, y1);
-        f2unpack(y23, y2, y3);
-        pk[c / 2] = pack_bf16x2(y0, y1);
-        pk[c / 2 + 1] = pack_bf16x2(y2, y3);
+        f2unpack(fadd2(f2pack(dv[c], dv[c + 1]), f2pack(nd.x, nd.y)), dv[c], dv[c + 1]);
+        f2unpack(fadd2(f2pack(dv[c + 2], dv[c + 3]), f2pack(nd.z, nd.w)), dv[c + 2], dv[c + 3]);
       }
-      tmem_st_x32(tDP, pk);
+      tmem_st_x16(tDP, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(W_P + g));
+#pragma unroll
+      for (int c = 0; c < kBwdCols; c += 2) {
+        float y0, y1;
+        f2unpack(fmul2(f2pack(pv[c], pv[c + 1]), f2pack(dv[c], dv[c + 1])), y0, y1);
+        pk[c / 2] = pack_bf16x2(y0, y1);
+      }
+      tmem_st_x16(tDP + kBwdCols / 2, pk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(W_DS + g));
     }
-    // epilogue: group 0 writes dV (through V's tile), group 1 dK (through K's)
+    // epilogue: groups 0 and 1 write dV (through V's tile), 2 and 3 dK (through
+    // K's), 64 channels each
     if (n > 0) {
       ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(W_FINAL), 0, limit));
       tc_fence_after();
       mbar_wait(bar(W_AB), 0, limit);                   // the tile has landed before it is written over
     }
     const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
-    const uint32_t sOut = base + (g ? L::kA : L::kB);
-    store_rows<D>(tbase + lane_off + (g ? kTDK : kTDV), sOut, r, g ? p.scale : 1.f, have);
-    fence_proxy_async_smem();
-    named_barrier_sync(1 + g, 128);
-    if (r == 0) {
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) tma_store_3d(g ? &tmDK : &tmDV, sOut + b * L::kBox, b * 64, h, kt * 128);
-      bulk_commit();
-      bulk_wait_read_all();
+    const int acc = g >> 1, b = g & 1;
+    if (b * 64 < D) {
+      const uint32_t sOut = base + (acc ? L::kA : L::kB) + b * L::kBox;
+      store_rows(tbase + lane_off + (acc ? kTDK : kTDV) + b * 64, sOut, r, acc ? p.scale : 1.f, have);
+      fence_proxy_async_smem();
+      named_barrier_sync(1 + g, 128);
+      if (r == 0) {
+        tma_store_3d(acc ? &tmDK : &tmDV, sOut, b * 64, h, kt * 128);
+        bulk_commit();
+        bulk_wait_read_all();
+      }
     }
   }
   tc_fence_before();
@@ -501,7 +542,16 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   }
 }
 
-enum : int { X_AB = 0, X_KFULL = 1, X_KEMPTY = 4, X_VFULL = 7, X_VEMPTY = 9, X_SFULL = 11, X_DPFULL = 13, X_DS = 14, X_FINAL = 16 };
+enum : int {
+  X_AB = 0,                           // Q and dO loaded
+  X_KFULL = 1, X_KEMPTY = 4,          // [3]
+  X_VFULL = 7, X_VEMPTY = 9,          // [2]
+  X_SFULL = 11,                       // [2]
+  X_DPFULL = 13,
+  X_DS = 14,                          // [group]
+  X_FINAL = X_DS + kBwdGroups,
+  X_COUNT
+};
 
 // dQ of one query tile.
 template <int D>
@@ -510,12 +560,15 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                    const __grid_constant__ CUtensorMap tmDQ, const BwdParams p) {
   using L = BwdSmem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_bwd[];
+  const uint32_t base = smem_u32(smem_bwd);
+  if (base & 1023u) {                                   // the swizzled tiles need the declared alignment
+    set_status(BSA_ERR_CUDA);
+    return;
+  }
   const uint32_t bar0 = base + L::kBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_raw + (base - raw) + L::kHolder);
+  volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_bwd + L::kHolder);
 
   const int qt = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -533,7 +586,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i <= X_FINAL; ++i) mbar_init(bar(i), (i >= X_DS && i < X_FINAL) ? 4 : 1);
+    for (int i = 0; i < X_COUNT; ++i) mbar_init(bar(i), (i >= X_DS && i < X_FINAL) ? 4 : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -547,10 +600,11 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   constexpr uint32_t kTDP = 256, kTDQ = 384;                  // S_0 at 0, S_1 at 128
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescD = idesc_bf16_f32(128, D, false, true);
-  auto sK = [&](int j) -> uint32_t { return base + L::kRing + (j % 3) * L::kTile; };
-  auto sV = [&](int j) -> uint32_t { return base + L::kRing + (3 + (j & 1)) * L::kTile; };
+  auto sK = [&](int j) -> uint32_t { return base + L::kRing3 + (j % 3) * L::kTile; };
+  auto sV = [&](int j) -> uint32_t { return base + L::kRing2 + (j & 1) * L::kTile; };
 
   if (warp == 0) {
+    regs_dec<kBwdRegsLow>();
     if (lane == 0 && n > 0) {
       mbar_arrive_expect_tx(bar(X_AB), 2 * L::kTile);
 #pragma unroll
@@ -583,6 +637,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       for (int u = max(0, jv - 2); u < jv; ++u) mbar_wait(bar(X_VFULL + (u & 1)), (u >> 1) & 1, limit);
     }
   } else if (warp == 1) {
+    regs_dec<kBwdRegsLow>();
     if (n > 0) {
       const uint64_t dQ = desc64(sw128_desc(base + L::kA, 16, 1024)), dG = desc64(sw128_desc(base + L::kB, 16, 1024));
       // S = Q K_j^T into buffer j % 2
@@ -618,27 +673,32 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       if (ok && n > 1 && (ok = k_wait(1))) s_mma(1);
       for (int j = 0; ok && j < n; ++j) {
         if (j + 1 < n && !(ok = v_wait(j + 1))) break;
-        // dS_j of both halves: dP has been read and S_j is done with
         const uint64_t dk = desc64(sw128_desc(sK(j), L::kBox, 1024));
         const uint32_t tA = tbase + (j & 1) * 128;
-        if (!(ok = mbar_wait_warp(bar(X_DS), j & 1, limit))) break;
-        if (!(ok = mbar_wait_warp(bar(X_DS + 1), j & 1, limit))) break;
+        // dS_j of every group: dP has been read and S_j is done with
+#pragma unroll
+        for (int g = 0; g < kBwdGroups; ++g) ok = mbar_wait_warp(bar(X_DS + g), j & 1, limit) && ok;
+        if (!ok) break;
         tc_fence_after();
         if (j + 1 < n) dp_mma(j + 1);
         // dQ += dS K_j
-        mma4_ts_warp(tbase + kTDQ, tA, dk, kIdescD, j > 0);
-        mma4_ts_warp(tbase + kTDQ, tA + 64, dk + 512, kIdescD, 1u);
+#pragma unroll
+        for (int g = 0; g < kBwdGroups; ++g)
+          mma2_ts_warp(tbase + kTDQ, tA + g * kBwdCols, dk + g * (kBwdCols * 128 >> 4), kIdescD, (j > 0 || g > 0) ? 1u : 0u);
         tc_commit_warp(bar(X_KEMPTY + j % 3));
         if (j + 2 < n && (ok = k_wait(j + 2))) s_mma(j + 2);
       }
       tc_commit_warp(bar(X_FINAL));
       mbar_wait_warp(bar(X_FINAL), 0, limit);
     }
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    regs_dec<kBwdRegsLow>();
+  } else {
+    regs_inc<kBwdRegsHigh>();
     const int g = (warp - 4) >> 2;
     const int r = (threadIdx.x - 128) & 127;
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tDP = tbase + lane_off + kTDP + 64 * g;
+    const uint32_t tDP = tbase + lane_off + kTDP + kBwdCols * g;
     const int fq = p.fbits != nullptr ? min(qt * 128 + r, p.N - 1) / p.P : 0;
     const float nl = p.nl[static_cast<size_t>(h) * NP + qt * 128 + r], nd = p.nd[static_cast<size_t>(h) * NP + qt * 128 + r];
     const uint64_t sl2p = f2pack(p.sl2, p.sl2), nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
@@ -655,17 +715,17 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       if (kt < 0 || kt >= p.nB) continue;
       const bool part = flg != nullptr ? fl != 0u : kt * 128 + 128 > p.N;
-      uint32_t mw[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-      if (part) key_mask(p, fq, kt * 128 + 64 * g, mw);
-      const uint32_t tS = tbase + lane_off + (j & 1) * 128 + 64 * g;
+      uint32_t mw = 0xFFFFFFFFu;
+      if (part) mw = key_mask(p, fq, kt * 128 + kBwdCols * g);
+      const uint32_t tS = tbase + lane_off + (j & 1) * 128 + kBwdCols * g;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(X_SFULL + (j & 1)), (j >> 1) & 1, limit));
       if (!ok) break;
       tc_fence_after();
-      uint32_t sr[64];
+      uint32_t sr[32];
       float* pv = reinterpret_cast<float*>(sr);
-      tmem_ld_x64(tS, sr);
+      tmem_ld_x32(tS, sr);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < kBwdCols; c += 2) {
         float x0, x1;
         f2unpack(ffma2(f2pack(pv[c], pv[c + 1]), sl2p, nlp), x0, x1);
         pv[c] = ex2_approx(x0);
@@ -673,37 +733,37 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
       if (part) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!((mw[c >> 5] >> (c & 31)) & 1u)) pv[c] = 0.f;
+        for (int c = 0; c < kBwdCols; ++c)
+          if (!((mw >> c) & 1u)) pv[c] = 0.f;
       }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(X_DPFULL), j & 1, limit));
       if (!ok) break;
       tc_fence_after();
-      uint32_t dr[64], pk[32];
+      uint32_t dr[32], pk[16];
       const float* dv = reinterpret_cast<const float*>(dr);
-      tmem_ld_x64(tDP, dr);
+      tmem_ld_x32(tDP, dr);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
+      for (int c = 0; c < kBwdCols; c += 2) {
         float y0, y1;
         f2unpack(fmul2(f2pack(pv[c], pv[c + 1]), fadd2(f2pack(dv[c], dv[c + 1]), ndp)), y0, y1);
         pk[c / 2] = pack_bf16x2(y0, y1);
       }
-      tmem_st_x32(tS, pk);
+      tmem_st_x16(tS, pk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(X_DS + g));
       ++j;
     }
-    // epilogue: each group writes half of dQ's channels through Q's tile
+    // epilogue: groups 0 and 1 write 64 channels of dQ each through Q's tile
     if (n > 0) {
       ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(X_FINAL), 0, limit));
       tc_fence_after();
       mbar_wait(bar(X_AB), 0, limit);
     }
     const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
-    if (D == 128 || g == 0) {
+    if (g * 64 < D) {
       const uint32_t sOut = base + L::kA + g * L::kBox;
-      store_rows<64>(tbase + lane_off + kTDQ + 64 * g, sOut, r, p.scale, have);
+      store_rows(tbase + lane_off + kTDQ + 64 * g, sOut, r, p.scale, have);
       fence_proxy_async_smem();
       named_barrier_sync(1 + g, 128);
       if (r == 0) {

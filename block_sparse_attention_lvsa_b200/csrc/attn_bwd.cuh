@@ -9,10 +9,10 @@
 // over the pairs that the index admits.  lse comes from the forward, so a
 // tile needs no running maximum and tiles can be taken in any grouping.
 //
-// Two kernels, each with every sum of its outputs inside one CTA (no atomics:
-// the result does not change from run to run), at the price of forming s and
-// <do, v> twice (7 products of 128 x 128 x d a tile instead of 5):
-//   attn_bwd_dkv_kernel  one CTA per 128-key tile and head, over the query
+// Two kinds of CTA in one launch, each with every sum of its outputs inside the
+// CTA (no atomics: the result does not change from run to run), at the price of
+// forming s and <do, v> twice (7 products of 128 x 128 x d a tile instead of 5):
+//   bwd_dkv  one CTA per 128-key tile and head, over the query
 //     tiles that list it (the index transposed on the device).  Tiles are
 //     held transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and dS^T
 //     (bf16, in TMEM) are the A operands of dV += P^T dO and dK += dS^T Q and
@@ -20,7 +20,7 @@
 //     each at d = 128): P and dS both lie over dP, so that S is free again as
 //     soon as its scores are in registers and the next tile's S runs during
 //     the exponentials.
-//   attn_bwd_dq_kernel   one CTA per 128-query tile and head, over its own
+//   bwd_dq   one CTA per 128-query tile and head, over its own
 //     list: S = Q K^T, dP = dO V^T, dQ += dS K.
 //
 // Warp roles (640 threads):
@@ -89,6 +89,13 @@ __device__ __forceinline__ void mma2_ts_warp(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate_first), "r"(1u)
       : "memory");
 }
+// 16 consecutive columns of the thread's TMEM lane, complete on return
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr) : "memory");
+}
 // 16 columns written and complete on return
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
@@ -111,40 +118,6 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
-}
-
-// nl = -lse * log2(e) and nd = -<do, o> per (head, token), [H][nB * 128];
-// tokens past N and rows without a key get nl = -inf (p = 0).  d/8 lanes a row.
-template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const __nv_bfloat16* __restrict__ o,
-                                                            long long o_ts, long long o_hs,
-                                                            const __nv_bfloat16* __restrict__ go,
-                                                            const float* __restrict__ lse, int N, int H, int NP,
-                                                            float* __restrict__ nl, float* __restrict__ nd) {
-  constexpr int G = D / 8;
-  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;   // n * H + h
-  const int l = threadIdx.x % G;
-  const long long n = row / H;
-  const int h = static_cast<int>(row - n * H);
-  float sum = 0.f;
-  if (n < N) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
-      sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
-    }
-  }
-#pragma unroll
-  for (int s = G / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-  if (l == 0 && n < NP) {
-    const size_t at = static_cast<size_t>(h) * NP + n;
-    const float e = n < N ? lse[static_cast<size_t>(h) * N + n] : -INFINITY;
-    nl[at] = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
-    nd[at] = -sum;
-  }
 }
 
 // Bit sets of the rows' lists: bits[h][w][qb] bit b = key tile 32 w + b is
@@ -193,30 +166,64 @@ __global__ void __launch_bounds__(128) attn_bwd_bits_kernel(const int32_t* __res
   if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(BSA_ERR_INDEX_RANGE);
 }
 
-// Query-tile lists of the key tiles, ascending.  One warp per 32 key tiles of
-// a head: lane = key tile, 32 query tiles' words per load.
-__global__ void __launch_bounds__(128) attn_bwd_lists_kernel(int nB, const uint32_t* __restrict__ bits,
-                                                             const uint32_t* __restrict__ part,
-                                                             int32_t* __restrict__ tlist, int32_t* __restrict__ tcount) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nW = (nB + 31) / 32;
-  const int w = blockIdx.x * 4 + warp, h = blockIdx.y;
-  if (w >= nW) return;
-  const int kt = w * 32 + lane;
-  const uint32_t* on = bits + (static_cast<size_t>(h) * nW + w) * nB;
-  const uint32_t* pt = part == nullptr ? nullptr : part + (static_cast<size_t>(h) * nW + w) * nB;
-  int32_t* out = tlist + (static_cast<size_t>(h) * nB + min(kt, nB - 1)) * nB;   // lanes past nB write nothing: their bits are 0
-  int n = 0;
-  for (int q0 = 0; q0 < nB; q0 += 32) {
-    const uint32_t a = q0 + lane < nB ? on[q0 + lane] : 0u;
-    const uint32_t b = (pt != nullptr && q0 + lane < nB) ? pt[q0 + lane] : 0u;
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t x = __shfl_sync(0xFFFFFFFFu, a, i), y = __shfl_sync(0xFFFFFFFFu, b, i);
-      if ((x >> lane) & 1u) out[n++] = (q0 + i) | (((y >> lane) & 1u) ? kPartialBit : 0);
+// Two independent preparations in one launch, 256 threads a block.
+// Blocks below `list_blocks`: the query-tile lists of the key tiles, ascending,
+// one warp per key tile of a head, 32 query tiles a step.
+// The others: nl = -lse * log2(e) and nd = -<do, o> per (head, token),
+// [H][nB * 128]; tokens past N and rows without a key get nl = -inf (p = 0);
+// d/8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_prep_kernel(
+    int nB, int list_heads, unsigned list_blocks, const uint32_t* __restrict__ bits, const uint32_t* __restrict__ part,
+    int32_t* __restrict__ tlist, int32_t* __restrict__ tcount, const __nv_bfloat16* __restrict__ o, long long o_ts,
+    long long o_hs, const __nv_bfloat16* __restrict__ go, const float* __restrict__ lse, int N, int H,
+    float* __restrict__ nl, float* __restrict__ nd) {
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x < list_blocks) {
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);   // h * nB + key tile
+    if (row >= static_cast<long long>(list_heads) * nB) return;
+    const int h = static_cast<int>(row / nB), kt = static_cast<int>(row - static_cast<long long>(h) * nB);
+    const size_t at = (static_cast<size_t>(h) * ((nB + 31) / 32) + (kt >> 5)) * nB;
+    int32_t* out = tlist + static_cast<size_t>(row) * nB;
+    int n = 0;
+    for (int q0 = 0; q0 < nB; q0 += 32) {
+      const int qb = q0 + lane;
+      const bool on = qb < nB && ((bits[at + qb] >> (kt & 31)) & 1u);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
+      if (on) {
+        const bool partial = part != nullptr && ((part[at + qb] >> (kt & 31)) & 1u);
+        out[n + __popc(m & ((1u << lane) - 1u))] = qb | (partial ? kPartialBit : 0);
+      }
+      n += __popc(m);
+    }
+    if (lane == 0) tcount[row] = n;
+    return;
+  }
+  constexpr int G = D / 8;
+  const int NP = nB * 128;
+  const long long row = (static_cast<long long>(blockIdx.x - list_blocks) * 256 + threadIdx.x) / G;   // n * H + h
+  const int l = threadIdx.x % G;
+  const int n = static_cast<int>(row / H);
+  const int h = static_cast<int>(row - static_cast<long long>(n) * H);
+  float sum = 0.f;
+  if (n < N) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+      sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
     }
   }
-  if (kt < nB) tcount[static_cast<size_t>(h) * nB + kt] = n;
+#pragma unroll
+  for (int s = G / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+  if (l == 0 && n < NP) {
+    const size_t at = static_cast<size_t>(h) * NP + n;
+    const float e = n < N ? lse[static_cast<size_t>(h) * N + n] : -INFINITY;
+    nl[at] = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
+    nd[at] = -sum;
+  }
 }
 
 __device__ __forceinline__ uint32_t bits32(int a, int b) {          // bits a .. b - 1, 0 <= a < b <= 32
@@ -244,26 +251,28 @@ __device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0)
   return m;
 }
 
-// 64 columns of one row of an f32 accumulator (TMEM) to bf16 in a
-// 128-byte-swizzled box in shared memory, times `mul`; zeros when !have.
-__device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sBox, int r, float mul, bool have) {
+// COLS columns of one row of an f32 accumulator (TMEM) to bf16 in a
+// 128-byte-swizzled box in shared memory, from its column `col`, times `mul`;
+// zeros when !have.
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint32_t tAcc, uint32_t sBox, int col, int r, float mul, bool have) {
 #pragma unroll
-  for (int c0 = 0; c0 < 64; c0 += 32) {
-    uint32_t ov[32];
+  for (int c0 = 0; c0 < COLS; c0 += 16) {
+    uint32_t ov[16];
     __syncwarp();
     if (have) {
-      tmem_ld_x32(tAcc + c0, ov);
+      tmem_ld_x16(tAcc + c0, ov);
     } else {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) ov[c] = 0u;
+      for (int c = 0; c < 16; ++c) ov[c] = 0u;
     }
 #pragma unroll
-    for (int v4 = 0; v4 < 4; ++v4) {
-      const uint32_t dst = sBox + r * 128 + (((c0 / 8 + v4) ^ (r & 7)) * 16);
+    for (int v = 0; v < 2; ++v) {
+      const uint32_t dst = sBox + r * 128 + ((((col + c0) / 8 + v) ^ (r & 7)) * 16);
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[i] = pack_bf16x2(__uint_as_float(ov[8 * v4 + 2 * i]) * mul, __uint_as_float(ov[8 * v4 + 2 * i + 1]) * mul);
+        w[i] = pack_bf16x2(__uint_as_float(ov[8 * v + 2 * i]) * mul, __uint_as_float(ov[8 * v + 2 * i + 1]) * mul);
       st_shared_v4(dst, w[0], w[1], w[2], w[3]);
     }
   }
@@ -288,20 +297,21 @@ enum : int {
   W_AB = 0,                           // K and V loaded
   W_QFULL = 1, W_QEMPTY = 4,          // [3]
   W_OFULL = 7, W_OEMPTY = 9,          // [2] dO, nl, nd
-  W_SFULL = 11, W_SFREE = 12, W_DPFULL = 13,
-  W_P = 14, W_DS = W_P + kBwdGroups,  // [group]
-  W_FINAL = W_DS + kBwdGroups,
+  W_SFULL = 11, W_SFREE = 12,
+  W_DPFULL = 13,                      // [2]
+  // [tile parity][group]: with two dP a group may store tile i+1 before the
+  // issuer has looked at another group's tile i
+  W_P = 15, W_DS = W_P + 2 * kBwdGroups,
+  W_FINAL = W_DS + 2 * kBwdGroups,
   W_COUNT
 };
 static_assert(W_COUNT <= 32, "barrier slots");
 
-// dK and dV of one key tile.
+// dK and dV of key tile kt of head h.
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-                    const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
-                    const BwdParams p) {
+__device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                        const CUtensorMap& tmG, const CUtensorMap& tmDK, const CUtensorMap& tmDV,
+                                        const BwdParams& p, const int kt, const int h) {
   using L = BwdSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_bwd[];
   const uint32_t base = smem_u32(smem_bwd);
@@ -313,7 +323,6 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_bwd + L::kHolder);
 
-  const int kt = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = p.wait_limit_ns;
   const int n = p.tcount[static_cast<size_t>(h) * p.tchs + kt];
@@ -324,6 +333,13 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     for (int i = 0; i < W_COUNT; ++i)
       mbar_init(bar(i), i == W_SFREE ? 4 * kBwdGroups : ((i >= W_P && i < W_FINAL) ? 4 : 1));
     fence_mbar_init();
+    // K and V are on their way while TMEM is allocated and the list is looked up
+    mbar_arrive_expect_tx(bar(W_AB), 2 * L::kTile);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      tma_load_3d(base + L::kA + b * L::kBox, &tmK, bar(W_AB), b * 64, h, kt * 128);
+      tma_load_3d(base + L::kB + b * L::kBox, &tmV, bar(W_AB), b * 64, h, kt * 128);
+    }
   }
   if (warp == 1) {
     tmem_alloc(base + L::kHolder, 512);
@@ -333,7 +349,10 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *holder;
-  constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 256, kTDK = 256 + D;
+  // d = 64 leaves room for two dP, so that dP(i+1) need not wait for dK(i)
+  constexpr int kDP = D == 64 ? 2 : 1;
+  constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 128 + 128 * kDP, kTDK = kTDV + D;
+  auto tdp = [&](int i) -> uint32_t { return tbase + kTDP + (kDP == 2 ? (i & 1) * 128u : 0u); };
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescD = idesc_bf16_f32(128, D, false, true);
   auto sQ = [&](int i) -> uint32_t { return base + L::kRing3 + (i % 3) * L::kTile; };
@@ -342,13 +361,7 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
   if (warp == 0) {
     regs_dec<kBwdRegsLow>();
-    if (lane == 0 && n > 0) {
-      mbar_arrive_expect_tx(bar(W_AB), 2 * L::kTile);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) {
-        tma_load_3d(base + L::kA + b * L::kBox, &tmK, bar(W_AB), b * 64, h, kt * 128);
-        tma_load_3d(base + L::kB + b * L::kBox, &tmV, bar(W_AB), b * 64, h, kt * 128);
-      }
+    if (lane == 0) {
       int nq = 0, no = 0;                               // copies started
       bool ok = true;
       for (int i = 0; i < n; ++i) {
@@ -393,17 +406,17 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const uint64_t dg = desc64(sw128_desc(sG(i), 16, 1024));
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
-          mma4_ss_warp(tbase + kTDP, dV + g * (L::kBox >> 4), dg + g * (L::kBox >> 4), kIdescS, g > 0);
-        tc_commit_warp(bar(W_DPFULL));
+          mma4_ss_warp(tdp(i), dV + g * (L::kBox >> 4), dg + g * (L::kBox >> 4), kIdescS, g > 0);
+        tc_commit_warp(bar(W_DPFULL + (kDP == 2 ? (i & 1) : 0)));
       };
       // dst += A^T B, 32 queries of A (in dP's columns from `off`) as each group stores them
       auto grad_mma = [&](uint32_t dst, uint32_t off, uint32_t tile, int first_bar, int i) -> bool {
         const uint64_t db = desc64(sw128_desc(tile, L::kBox, 1024));
 #pragma unroll
         for (int g = 0; g < kBwdGroups; ++g) {
-          if (!mbar_wait_warp(bar(first_bar + g), i & 1, limit)) return false;
+          if (!mbar_wait_warp(bar(first_bar + (i & 1) * kBwdGroups + g), (i >> 1) & 1, limit)) return false;
           tc_fence_after();
-          mma2_ts_warp(tbase + dst, tbase + kTDP + off + g * kBwdCols, db + g * (kBwdCols * 128 >> 4), kIdescD,
+          mma2_ts_warp(tbase + dst, tdp(i) + off + g * kBwdCols, db + g * (kBwdCols * 128 >> 4), kIdescD,
                        (i > 0 || g > 0) ? 1u : 0u);
         }
         return true;
@@ -422,13 +435,18 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           if (!(ok = mbar_wait_warp(bar(W_SFREE), i & 1, limit))) break;
           tc_fence_after();
           s_mma(nx);
+          if (kDP == 2) {
+            if (!(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+            tc_fence_after();
+            dp_mma(nx);
+          }
         }
         if (!(ok = grad_mma(kTDV, 0, sG(i), W_P, i))) break;                       // dV += P^T dO_i
         tc_commit_warp(bar(W_OEMPTY + (i & 1)));
-        if (nx < n && !(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
+        if (kDP == 1 && nx < n && !(ok = mbar_wait_warp(bar(W_OFULL + (nx & 1)), (nx >> 1) & 1, limit))) break;
         if (!(ok = grad_mma(kTDK, kBwdCols / 2, sQ(i), W_DS, i))) break;           // dK += dS^T Q_i
         tc_commit_warp(bar(W_QEMPTY + i % 3));
-        if (nx < n) dp_mma(nx);
+        if (kDP == 1 && nx < n) dp_mma(nx);
       }
       tc_commit_warp(bar(W_FINAL));
       mbar_wait_warp(bar(W_FINAL), 0, limit);
@@ -440,7 +458,7 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int g = (warp - 4) >> 2;
     const int r = (threadIdx.x - 128) & 127;
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tS = tbase + lane_off + kTS + kBwdCols * g, tDP = tbase + lane_off + kTDP + kBwdCols * g;
+    const uint32_t tS = tbase + lane_off + kTS + kBwdCols * g, tDP0 = lane_off + kBwdCols * g;
     const int fk = p.fbits != nullptr ? min(kt * 128 + r, p.N - 1) / p.P : 0;
     const uint64_t sl2p = f2pack(p.sl2, p.sl2);
     bool ok = true;
@@ -468,13 +486,10 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const float4 nl = ld_shared_f4(rowv + 4 * c);
         const uint64_t x01 = ffma2(f2pack(pv[c], pv[c + 1]), sl2p, f2pack(nl.x, nl.y));
         const uint64_t x23 = ffma2(f2pack(pv[c + 2], pv[c + 3]), sl2p, f2pack(nl.z, nl.w));
-        float x0, x1, x2, x3;
-        f2unpack(x01, x0, x1);
-        f2unpack(x23, x2, x3);
-        pv[c] = ex2_approx(x0);
-        pv[c + 1] = ex2_approx(x1);
-        pv[c + 2] = ex2_approx(x2);
-        pv[c + 3] = ex2_approx(x3);
+        f2unpack(x01, pv[c], pv[c + 1]);
+        f2unpack(x23, pv[c + 2], pv[c + 3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pv[c + u] = ex2_approx(pv[c + u]);
       }
       if (part) {
 #pragma unroll
@@ -483,11 +498,12 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
 #pragma unroll
       for (int c = 0; c < kBwdCols; c += 2) pk[c / 2] = pack_bf16x2(pv[c], pv[c + 1]);
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_DPFULL), i & 1, limit));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_DPFULL + (kDP == 2 ? (i & 1) : 0)), (kDP == 2 ? i >> 1 : i) & 1, limit));
       if (!ok) break;
       tc_fence_after();
       // dP of these columns goes to registers, P takes the first half of them,
       // dS the second; nd is read before P is signalled, which lets go of the rows
+      const uint32_t tDP = tdp(i) + tDP0;
       uint32_t dr[32];
       float* dv = reinterpret_cast<float*>(dr);
       tmem_ld_x32(tDP, dr);
@@ -500,7 +516,7 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       tmem_st_x16(tDP, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(W_P + g));
+      if (lane == 0) mbar_arrive(bar(W_P + (i & 1) * kBwdGroups + g));
 #pragma unroll
       for (int c = 0; c < kBwdCols; c += 2) {
         float y0, y1;
@@ -510,20 +526,20 @@ attn_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       tmem_st_x16(tDP + kBwdCols / 2, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(W_DS + g));
+      if (lane == 0) mbar_arrive(bar(W_DS + (i & 1) * kBwdGroups + g));
     }
     // epilogue: groups 0 and 1 write dV (through V's tile), 2 and 3 dK (through
     // K's), 64 channels each
     if (n > 0) {
       ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(W_FINAL), 0, limit));
       tc_fence_after();
-      mbar_wait(bar(W_AB), 0, limit);                   // the tile has landed before it is written over
     }
+    __all_sync(0xFFFFFFFFu, mbar_wait(bar(W_AB), 0, limit));   // the tile has landed before it is written over
     const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
     const int acc = g >> 1, b = g & 1;
     if (b * 64 < D) {
       const uint32_t sOut = base + (acc ? L::kA : L::kB) + b * L::kBox;
-      store_rows(tbase + lane_off + (acc ? kTDK : kTDV) + b * 64, sOut, r, acc ? p.scale : 1.f, have);
+      store_rows<64>(tbase + lane_off + (acc ? kTDK : kTDV) + b * 64, sOut, 0, r, acc ? p.scale : 1.f, have);
       fence_proxy_async_smem();
       named_barrier_sync(1 + g, 128);
       if (r == 0) {
@@ -548,17 +564,16 @@ enum : int {
   X_VFULL = 7, X_VEMPTY = 9,          // [2]
   X_SFULL = 11,                       // [2]
   X_DPFULL = 13,
-  X_DS = 14,                          // [group]
-  X_FINAL = X_DS + kBwdGroups,
+  X_DS = 14,
+  X_FINAL = 15,
   X_COUNT
 };
 
-// dQ of one query tile.
+// dQ of query tile qt of head h.
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-                   const __grid_constant__ CUtensorMap tmDQ, const BwdParams p) {
+__device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                       const CUtensorMap& tmG, const CUtensorMap& tmDQ, const BwdParams& p,
+                                       const int qt, const int h) {
   using L = BwdSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_bwd[];
   const uint32_t base = smem_u32(smem_bwd);
@@ -570,10 +585,20 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
   volatile uint32_t* holder = reinterpret_cast<volatile uint32_t*>(smem_bwd + L::kHolder);
 
-  const int qt = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = p.wait_limit_ns;
   const int NP = p.nB * 128;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < X_COUNT; ++i) mbar_init(bar(i), i == X_DS ? 4 * kBwdGroups : 1);
+    fence_mbar_init();
+    // Q and dO are on their way while the list is looked up
+    mbar_arrive_expect_tx(bar(X_AB), 2 * L::kTile);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      tma_load_3d(base + L::kA + b * L::kBox, &tmQ, bar(X_AB), b * 64, h, qt * 128);
+      tma_load_3d(base + L::kB + b * L::kBox, &tmG, bar(X_AB), b * 64, h, qt * 128);
+    }
+  }
   int m = p.count[static_cast<size_t>(h) * p.chs + qt];       // entries; n: those in range
   m = min(max(m, 0), p.lrs);
   const size_t off = static_cast<size_t>(h) * p.lhs + static_cast<size_t>(qt) * p.lrs;
@@ -585,10 +610,6 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     n += __popc(__ballot_sync(0xFFFFFFFFu, e >= 0 && e < p.nB));
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < X_COUNT; ++i) mbar_init(bar(i), (i >= X_DS && i < X_FINAL) ? 4 : 1);
-    fence_mbar_init();
-  }
   if (warp == 1) {
     tmem_alloc(base + L::kHolder, 512);
     tmem_relinquish();
@@ -605,13 +626,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   if (warp == 0) {
     regs_dec<kBwdRegsLow>();
-    if (lane == 0 && n > 0) {
-      mbar_arrive_expect_tx(bar(X_AB), 2 * L::kTile);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b) {
-        tma_load_3d(base + L::kA + b * L::kBox, &tmQ, bar(X_AB), b * 64, h, qt * 128);
-        tma_load_3d(base + L::kB + b * L::kBox, &tmG, bar(X_AB), b * 64, h, qt * 128);
-      }
+    if (lane == 0) {
       int jk = 0, jv = 0;
       bool ok = true;
       for (int u = 0; u < m; ++u) {
@@ -676,9 +691,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const uint64_t dk = desc64(sw128_desc(sK(j), L::kBox, 1024));
         const uint32_t tA = tbase + (j & 1) * 128;
         // dS_j of every group: dP has been read and S_j is done with
-#pragma unroll
-        for (int g = 0; g < kBwdGroups; ++g) ok = mbar_wait_warp(bar(X_DS + g), j & 1, limit) && ok;
-        if (!ok) break;
+        if (!(ok = mbar_wait_warp(bar(X_DS), j & 1, limit))) break;
         tc_fence_after();
         if (j + 1 < n) dp_mma(j + 1);
         // dQ += dS K_j
@@ -751,26 +764,27 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       tmem_st_x16(tS, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(X_DS + g));
+      if (lane == 0) mbar_arrive(bar(X_DS));
       ++j;
     }
-    // epilogue: groups 0 and 1 write 64 channels of dQ each through Q's tile
+    // epilogue: every group writes D / 4 channels of dQ through Q's tile
     if (n > 0) {
       ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(X_FINAL), 0, limit));
       tc_fence_after();
-      mbar_wait(bar(X_AB), 0, limit);
     }
+    __all_sync(0xFFFFFFFFu, mbar_wait(bar(X_AB), 0, limit));
     const bool have = __all_sync(0xFFFFFFFFu, ok && n > 0);
-    if (g * 64 < D) {
-      const uint32_t sOut = base + L::kA + g * L::kBox;
-      store_rows(tbase + lane_off + kTDQ + 64 * g, sOut, r, p.scale, have);
-      fence_proxy_async_smem();
-      named_barrier_sync(1 + g, 128);
-      if (r == 0) {
-        tma_store_3d(&tmDQ, sOut, g * 64, h, qt * 128);
-        bulk_commit();
-        bulk_wait_read_all();
-      }
+    constexpr int kCols = D / kBwdGroups;
+    const int c0 = g * kCols, b = c0 / 64;
+    const uint32_t sOut = base + L::kA + b * L::kBox;
+    store_rows<kCols>(tbase + lane_off + kTDQ + c0, sOut, c0 % 64, r, p.scale, have);
+    fence_proxy_async_smem();
+    constexpr int kPerBox = 64 / kCols;                 // groups that fill one box
+    named_barrier_sync(1 + b, 128 * kPerBox);
+    if (r == 0 && c0 % 64 == 0) {
+      tma_store_3d(&tmDQ, sOut, b * 64, h, qt * 128);
+      bulk_commit();
+      bulk_wait_read_all();
     }
   }
   tc_fence_before();
@@ -780,6 +794,21 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     __syncwarp();
     tmem_dealloc(tbase, 512);
   }
+}
+
+// grid (2 nB, heads): the key tiles of a head, then its query tiles, in one
+// launch, so that one kind fills the SMs that the other's last blocks leave.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
+                const __grid_constant__ CUtensorMap tmDV, const BwdParams p) {
+  const int t = blockIdx.x, h = blockIdx.y;
+  if (t < p.nB)
+    bwd_dkv<D>(tmQ, tmK, tmV, tmG, tmDK, tmDV, p, t, h);
+  else
+    bwd_dq<D>(tmQ, tmK, tmV, tmG, tmDQ, p, t - p.nB, h);
 }
 
 }  // namespace bsa

@@ -916,9 +916,8 @@ namespace {
 template <int D>
 int launch_bwd(const void* go, const void* q, const void* k, const void* v, int N, int H, const BwdParams& p,
                void* dq, void* dk, void* dv, cudaStream_t st) {
-  static std::atomic<bool> done_kv[kMaxDevices], done_q[kMaxDevices];
-  int rc = allow_smem(attn_bwd_dkv_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done_kv);
-  if (rc == BSA_OK) rc = allow_smem(attn_bwd_dq_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done_q);
+  static std::atomic<bool> done[kMaxDevices];
+  const int rc = allow_smem(attn_bwd_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done);
   if (rc != BSA_OK) return rc;
   CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
   if (!make_qkv_map(&mq, q, N, H, D, 128) || !make_qkv_map(&mk, k, N, H, D, 128) ||
@@ -926,9 +925,7 @@ int launch_bwd(const void* go, const void* q, const void* k, const void* v, int 
       !make_qkv_map(&mdq, dq, N, H, D, 128) || !make_qkv_map(&mdk, dk, N, H, D, 128) ||
       !make_qkv_map(&mdv, dv, N, H, D, 128))
     return BSA_ERR_CUDA;
-  const dim3 grid(p.nB, H);
-  attn_bwd_dkv_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdk, mdv, p);
-  attn_bwd_dq_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, p);
+  attn_bwd_kernel<D><<<dim3(2 * p.nB, H), kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, mdk, mdv, p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -974,7 +971,7 @@ extern "C" int blocksparse_attn_bwd(const void* go, const void* q, const void* k
   rc = setup_index(index, N, H, workspace, ws_bytes, a, &used, st);
   if (rc != BSA_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int nB = a.nB, nW = (nB + 31) / 32;
+  const int nB = a.nB;
   BwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.N = N;
@@ -1006,17 +1003,17 @@ extern "C" int blocksparse_attn_bwd(const void* go, const void* q, const void* k
   p.tchs = w.lists == 1 ? 0 : nB;
   attn_bwd_bits_kernel<<<dim3((nB + 3) / 4, w.lists), 128, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB,
                                                                    bits, part);
-  attn_bwd_lists_kernel<<<dim3((nW + 3) / 4, w.lists), 128, 0, st>>>(nB, bits, part, tlist, tcnt);
+  const unsigned list_blocks = static_cast<unsigned>((static_cast<long long>(w.lists) * nB + 7) / 8);
   const long long lanes = static_cast<long long>(nB) * 128 * H * (d / 8);
-  const unsigned blocks = static_cast<unsigned>((lanes + 255) / 256);
+  const unsigned blocks = list_blocks + static_cast<unsigned>((lanes + 255) / 256);
   const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o->data);
   const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(go);
   if (d == 128)
-    attn_bwd_rows_kernel<128><<<blocks, 256, 0, st>>>(ob, o->token_stride, o->head_stride, gb, lse, N, H, nB * 128,
-                                                    nl, nd);
+    attn_bwd_prep_kernel<128><<<blocks, 256, 0, st>>>(nB, w.lists, list_blocks, bits, part, tlist, tcnt, ob,
+                                                      o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
   else
-    attn_bwd_rows_kernel<64><<<blocks, 256, 0, st>>>(ob, o->token_stride, o->head_stride, gb, lse, N, H, nB * 128,
-                                                    nl, nd);
+    attn_bwd_prep_kernel<64><<<blocks, 256, 0, st>>>(nB, w.lists, list_blocks, bits, part, tlist, tcnt, ob,
+                                                     o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   return d == 128 ? launch_bwd<128>(go, q, k, v, N, H, p, dq, dk, dv, st)
                   : launch_bwd<64>(go, q, k, v, N, H, p, dq, dk, dv, st);

@@ -242,6 +242,22 @@ def test_repeats_stream_graph_and_workspace(bsa):
         bsa.blocksparse_attn_bwd(go, q, k, v, o, lse, bsa.block_index(idx[:, :15, :15].contiguous(), cnt[:, :15].contiguous()))
 
 
+def test_many_calls_in_a_row(bsa):
+    """The groups of threads run ahead of one another differently from call to
+    call; every call ends, with the same result (both head sizes, masks in every
+    tile)."""
+    for d in (64, 128):
+        T, P = 21, 157
+        go, q, k, v = make(T * P, 4, d, seed=85)
+        frames, counts, _ = bsa.lvsa_build_index(T, 5, 3, 7, 0, device="cuda")
+        ix = bsa.lvsa_index(T, frames, counts)
+        o, lse, ref = both(bsa, go, q, k, v, ix)
+        for _ in range(300):
+            got = bsa.blocksparse_attn_bwd(go, q, k, v, o, lse, ix)
+        assert bsa.get_device_status() == bsa.BSA_OK
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
 def test_against_differences_of_the_oracle(bsa):
     """Directional central differences of the float64 forward; the gradient's own
     tolerance is the bound above, summed along the direction."""

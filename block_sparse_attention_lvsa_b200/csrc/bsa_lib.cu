@@ -519,11 +519,24 @@ int check_sizes(int dtype, long long N, int d) {
   return BSA_OK;
 }
 
+// n / d = (n * m) >> s for 0 <= n < 2^31 and 1 <= d < 2^31: with 2^(l-1) < d <= 2^l
+// and m = floor(2^(31+l) / d) + 1 (33 bits at most; 32 because d > 2^(l-1)), m d
+// is above 2^(31+l) by at most 2^l, so that n m / 2^(31+l) is above n / d by less
+// than 1 / d.
+void division(uint32_t d, uint32_t* m, int* s) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  *m = static_cast<uint32_t>((1ull << (31 + l)) / d + 1);
+  *s = 31 + l;
+}
+
 // rope may be null: nothing is turned
 int rope_dev(const bsa_rope* rope, long long N, int d, bool inverse, RopeDev* r) {
   std::memset(r, 0, sizeof(*r));
   r->sign = inverse ? -1.f : 1.f;
   r->gh = r->gw = 1;
+  division(1, &r->mh, &r->sh);
+  division(1, &r->mw, &r->sw);
   if (!rope) return BSA_OK;
   if (rope->pairing != BSA_ROPE_ADJACENT && rope->pairing != BSA_ROPE_SPLIT) return BSA_ERR_ARG;
   long long sum = 0;
@@ -553,6 +566,8 @@ int rope_dev(const bsa_rope* rope, long long N, int d, bool inverse, RopeDev* r)
   }
   r->gh = rope->grid[1];
   r->gw = rope->grid[2];
+  division(r->gh, &r->mh, &r->sh);
+  division(r->gw, &r->mw, &r->sw);
   r->ngrid = n;
   return BSA_OK;
 }
@@ -568,23 +583,31 @@ void set_tensor(RopeTensor* t, const bsa_heads* x, const bsa_heads* g, const bsa
   t->yt = y->token_stride;
   t->yh = y->head_stride;
   t->H = y->H;
-  t->chunks = (y->H + kRopeHeads - 1) / kRopeHeads;
-  t->per = (y->H + t->chunks - 1) / t->chunks;
-  t->chunks = (y->H + t->per - 1) / t->per;
   t->w = w;
 }
 
-// blocks that hold every group of the larger tensor, at most `most`
-unsigned rope_blocks(const RopeParams& p, int tensors, int d, long long most) {
+// Grid of a rotation: blocks over the tokens (at most `most` in all, each then
+// strides), tensors, parts of the heads.  A block takes all heads of its tokens,
+// so that their angles are looked up once; with too few tokens to fill the
+// SMs the heads are dealt to several blocks, kRopeHeads at the least.
+dim3 rope_grid(RopeParams* p, int tensors, int d, long long most) {
   const int groups = kRopeThreads / (d / 8);
-  long long b = 1;
-  for (int i = 0; i < tensors; ++i) b = std::max(b, (p.N * p.t[i].chunks + groups - 1) / groups);
-  return static_cast<unsigned>(std::min(b, most));
+  int H = 1;
+  for (int i = 0; i < tensors; ++i) H = std::max(H, p->t[i].H);
+  const long long blocks = (p->N + groups - 1) / groups;
+  p->per = H;
+  int parts = 1;
+  while (p->per > kRopeHeads && blocks * tensors * parts < 2 * 148) {
+    p->per = std::max(kRopeHeads, (p->per / 2 + kRopeHeads - 1) / kRopeHeads * kRopeHeads);
+    parts = (H + p->per - 1) / p->per;
+  }
+  const long long x = std::max(1LL, std::min(blocks, most / (static_cast<long long>(tensors) * parts)));
+  return dim3(static_cast<unsigned>(x), tensors, parts);
 }
 
 template <typename T, int D>
-int launch_rope_fwd(const RopeParams& p, int tensors, bool split, bool norm, cudaStream_t st) {
-  const dim3 grid(rope_blocks(p, tensors, D, 1LL << 30), tensors);
+int launch_rope_fwd(RopeParams& p, int tensors, bool split, bool norm, cudaStream_t st) {
+  const dim3 grid = rope_grid(&p, tensors, D, 148 * 3 * 4);
   if (split) {
     if (norm) rope_fwd_kernel<T, D, true, true><<<grid, kRopeThreads, 0, st>>>(p);
     else rope_fwd_kernel<T, D, true, false><<<grid, kRopeThreads, 0, st>>>(p);
@@ -595,7 +618,7 @@ int launch_rope_fwd(const RopeParams& p, int tensors, bool split, bool norm, cud
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
-int launch_rope_fwd_any(const RopeParams& p, int dtype, int d, int tensors, bool split, bool norm, cudaStream_t st) {
+int launch_rope_fwd_any(RopeParams& p, int dtype, int d, int tensors, bool split, bool norm, cudaStream_t st) {
   if (d == 128) {
     if (dtype == BSA_BF16) return launch_rope_fwd<__nv_bfloat16, 128>(p, tensors, split, norm, st);
     if (dtype == BSA_F16) return launch_rope_fwd<__half, 128>(p, tensors, split, norm, st);
@@ -606,28 +629,26 @@ int launch_rope_fwd_any(const RopeParams& p, int dtype, int d, int tensors, bool
   return launch_rope_fwd<float, 64>(p, tensors, split, norm, st);
 }
 
-// most blocks of the backward pass: their weight-gradient partial sums are
-// added by one block per tensor afterwards
+// most blocks of the backward pass (all tensors and parts of the heads): their
+// weight-gradient partial sums are added by one block per tensor afterwards
 constexpr long long kRopeBwdBlocks = 148 * 4;
 
 template <typename T, int D>
-int launch_rope_bwd(const RopeParams& p, int tensors, bool split, unsigned blocks, cudaStream_t st) {
-  const dim3 grid(blocks, tensors);
+int launch_rope_bwd(const RopeParams& p, bool split, dim3 grid, cudaStream_t st) {
   if (split) rope_bwd_kernel<T, D, true><<<grid, kRopeThreads, 0, st>>>(p);
   else rope_bwd_kernel<T, D, false><<<grid, kRopeThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
-int launch_rope_bwd_any(const RopeParams& p, int dtype, int d, int tensors, bool split, unsigned blocks,
-                        cudaStream_t st) {
+int launch_rope_bwd_any(const RopeParams& p, int dtype, int d, bool split, dim3 grid, cudaStream_t st) {
   if (d == 128) {
-    if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 128>(p, tensors, split, blocks, st);
-    if (dtype == BSA_F16) return launch_rope_bwd<__half, 128>(p, tensors, split, blocks, st);
-    return launch_rope_bwd<float, 128>(p, tensors, split, blocks, st);
+    if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 128>(p, split, grid, st);
+    if (dtype == BSA_F16) return launch_rope_bwd<__half, 128>(p, split, grid, st);
+    return launch_rope_bwd<float, 128>(p, split, grid, st);
   }
-  if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 64>(p, tensors, split, blocks, st);
-  if (dtype == BSA_F16) return launch_rope_bwd<__half, 64>(p, tensors, split, blocks, st);
-  return launch_rope_bwd<float, 64>(p, tensors, split, blocks, st);
+  if (dtype == BSA_BF16) return launch_rope_bwd<__nv_bfloat16, 64>(p, split, grid, st);
+  if (dtype == BSA_F16) return launch_rope_bwd<__half, 64>(p, split, grid, st);
+  return launch_rope_bwd<float, 64>(p, split, grid, st);
 }
 
 // weight type and pointers of the norm
@@ -698,7 +719,10 @@ int qk_norm_rope_fwd(const bsa_heads* q, const bsa_heads* k, const bsa_heads* qo
 
 size_t qk_norm_rope_bwd_workspace_bytes(long long N, int Hq, int Hk, int d) {
   if (N < 1 || Hq < 1 || Hk < 0 || (d != 64 && d != 128)) return static_cast<size_t>(-1);
-  return static_cast<size_t>(2) * kRopeBwdBlocks * d * sizeof(float);
+    // the grid's parts of the heads number at most ceil(H / kRopeHeads), a tensor's
+  // blocks at least one each
+  const size_t parts = static_cast<size_t>(std::max(Hq, Hk) + kRopeHeads - 1) / kRopeHeads;
+  return std::max<size_t>(kRopeBwdBlocks, 2 * parts) * d * sizeof(float);
 }
 
 int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* q, const bsa_heads* k,
@@ -734,10 +758,10 @@ int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* 
   if (k) set_tensor(&p.t[1], k, gk, dk, wk);
   p.partial = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = rope_blocks(p, tensors, d, kRopeBwdBlocks);
-  rc = launch_rope_bwd_any(p, dtype, d, tensors, rope && rope->pairing == BSA_ROPE_SPLIT, blocks, st);
+  const dim3 grid = rope_grid(&p, tensors, d, kRopeBwdBlocks);
+  rc = launch_rope_bwd_any(p, dtype, d, rope && rope->pairing == BSA_ROPE_SPLIT, grid, st);
   if (rc != BSA_OK || (!dwq && !dwk)) return rc;
-  rope_dw_kernel<<<tensors, 1024, 0, st>>>(p.partial, static_cast<int>(blocks), d, dwq, dwk);
+  rope_dw_kernel<<<tensors, 1024, 0, st>>>(p.partial, static_cast<int>(grid.x * grid.z), d, dwq, dwk);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

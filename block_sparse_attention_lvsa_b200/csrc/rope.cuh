@@ -20,18 +20,26 @@
 // neighbouring lanes own one row, four pairs (eight channels) a lane, so both
 // members of a pair, the table entries and the weights of a lane's channels
 // stay in that lane; the row sums are butterflies over d/8 lanes.  A group of
-// d/8 lanes takes up to kRopeHeads heads of one token: their loads are all
-// issued before the first use, and the lane's four (cos, sin) are read once
-// for all of them.  All arithmetic is float32; the one rounding is the
-// store.
+// d/8 lanes goes through the heads of one token, kRopeHeads rows' loads at a
+// time, with the token's cos and sin (times the weights) in registers, and the
+// blocks stride over the tokens, so that a lane finds its pairs once.  The
+// arithmetic is in packed pairs of float32 (half the instructions: with scalar
+// ones and one token and eight heads a block the kernel was bound by
+// instruction issue, NEW1); the one rounding is the store.
 #pragma once
 #include <cuda_fp16.h>
-#include "ptx.cuh"
+#include "attn_fwd.cuh"
 
 namespace bsa {
 
-constexpr int kRopeHeads = 8;        // most heads per group and step
+constexpr int kRopeHeads = 4;        // rows of a group whose loads are in flight
 constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // Device view of bsa_rope.
 struct RopeDev {
@@ -39,7 +47,9 @@ struct RopeDev {
   int pairs[3];
   int len[3];
   int first[3];
-  int gh, gw;                        // grid height and width
+  uint32_t gh, gw;                   // grid height and width
+  uint32_t mh, mw;                   // n / gh = (n * mh) >> sh for 0 <= n < 2^31, and so for gw
+  int sh, sw;
   long long ngrid;                   // tokens inside the grid
   const int32_t* pos;                // [N][3] or null (grid)
   float sign;                        // +1 forward, -1 inverse
@@ -52,8 +62,6 @@ struct RopeTensor {
   void* y;                           // output / input gradient
   long long xt, xh, gt, gh, yt, yh;  // token and head strides
   int H;
-  int chunks;                        // groups a token's heads are dealt to
-  int per;                           // heads per group: ceil(H / chunks)
   const void* w;                     // norm weight [d] or null
 };
 
@@ -61,22 +69,24 @@ struct RopeParams {
   RopeTensor t[2];                   // q, k (blockIdx.y)
   long long N;
   RopeDev r;
+  int per;                           // heads per block of a token (blockIdx.z counts them)
   int w_f32;                         // weights are float32 (else the tensors' type)
   float eps;
-  float* partial;                    // backward: [2][gridDim.x][d] weight-gradient partial sums
+  float* partial;                    // backward: [2][gridDim.x * gridDim.z][d] weight-gradient partial sums
 };
 
-// eight channels of a row as float: adjacent layout = 8 consecutive channels,
-// split layout = 4 at c and 4 at c + d/2; member a of pair u is v[2u], b v[2u+1]
-template <typename T> struct Vec8;
+// A lane's eight channels as loaded: adjacent layout 8 consecutive channels,
+// split layout 4 at c and 4 at c + d/2.
+template <typename T> struct Vec8 {
+  uint2 a, b;
+};
 template <> struct Vec8<float> {
   float4 a, b;
 };
-template <> struct Vec8<__nv_bfloat16> {
-  uint2 a, b;
-};
-template <> struct Vec8<__half> {
-  uint2 a, b;
+// The same as packed pairs of float: members a of pairs (0, 1) and (2, 3),
+// members b of the same pairs.
+struct Row8 {
+  uint64_t a[2], b[2];
 };
 
 template <bool SPLIT, int D>
@@ -108,46 +118,58 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// f[0..7] in pair order: f[2u], f[2u+1] are the two members of pair u
 template <bool SPLIT>
-__device__ __forceinline__ void to_pairs(const Vec8<float>& v, float (&f)[8]) {
-  const float x[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    f[2 * u] = SPLIT ? x[u] : x[2 * u];
-    f[2 * u + 1] = SPLIT ? x[4 + u] : x[2 * u + 1];
+__device__ __forceinline__ Row8 to_row(const Vec8<float>& v) {
+  Row8 r;
+  if (SPLIT) {
+    r.a[0] = f2pack(v.a.x, v.a.y);
+    r.a[1] = f2pack(v.a.z, v.a.w);
+    r.b[0] = f2pack(v.b.x, v.b.y);
+    r.b[1] = f2pack(v.b.z, v.b.w);
+  } else {
+    r.a[0] = f2pack(v.a.x, v.a.z);
+    r.a[1] = f2pack(v.b.x, v.b.z);
+    r.b[0] = f2pack(v.a.y, v.a.w);
+    r.b[1] = f2pack(v.b.y, v.b.w);
   }
+  return r;
 }
 template <bool SPLIT, typename T>
-__device__ __forceinline__ void to_pairs(const Vec8<T>& v, float (&f)[8]) {
-  const float2 p[4] = {unpack2(v.a.x, T()), unpack2(v.a.y, T()), unpack2(v.b.x, T()), unpack2(v.b.y, T())};
-  const float x[8] = {p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    f[2 * u] = SPLIT ? x[u] : x[2 * u];
-    f[2 * u + 1] = SPLIT ? x[4 + u] : x[2 * u + 1];
+__device__ __forceinline__ Row8 to_row(const Vec8<T>& v) {
+  const float2 p = unpack2(v.a.x, T()), q = unpack2(v.a.y, T()), s = unpack2(v.b.x, T()), t = unpack2(v.b.y, T());
+  Row8 r;
+  if (SPLIT) {
+    r.a[0] = f2pack(p.x, p.y);
+    r.a[1] = f2pack(q.x, q.y);
+    r.b[0] = f2pack(s.x, s.y);
+    r.b[1] = f2pack(t.x, t.y);
+  } else {
+    r.a[0] = f2pack(p.x, q.x);
+    r.a[1] = f2pack(s.x, t.x);
+    r.b[0] = f2pack(p.y, q.y);
+    r.b[1] = f2pack(s.y, t.y);
   }
+  return r;
 }
 
-template <bool SPLIT, int D>
-__device__ __forceinline__ void store8(float* row, int l, const float (&f)[8]) {
-  float x[8];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    x[SPLIT ? u : 2 * u] = f[2 * u];
-    x[SPLIT ? 4 + u : 2 * u + 1] = f[2 * u + 1];
-  }
-  *reinterpret_cast<float4*>(row + (SPLIT ? 4 * l : 8 * l)) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(row + (SPLIT ? D / 2 + 4 * l : 8 * l + 4)) = make_float4(x[4], x[5], x[6], x[7]);
-}
 template <bool SPLIT, int D, typename T>
-__device__ __forceinline__ void store8(T* row, int l, const float (&f)[8]) {
-  if (SPLIT) {
-    *reinterpret_cast<uint2*>(row + 4 * l) = make_uint2(pack2(f[0], f[2], T()), pack2(f[4], f[6], T()));
-    *reinterpret_cast<uint2*>(row + D / 2 + 4 * l) = make_uint2(pack2(f[1], f[3], T()), pack2(f[5], f[7], T()));
+__device__ __forceinline__ void store8(T* row, int l, const Row8& r) {
+  float a[4], b[4];
+  f2unpack(r.a[0], a[0], a[1]);
+  f2unpack(r.a[1], a[2], a[3]);
+  f2unpack(r.b[0], b[0], b[1]);
+  f2unpack(r.b[1], b[2], b[3]);
+  if constexpr (sizeof(T) == 4) {
+    float4* p = reinterpret_cast<float4*>(row + (SPLIT ? 4 * l : 8 * l));
+    float4* q = reinterpret_cast<float4*>(row + (SPLIT ? D / 2 + 4 * l : 8 * l + 4));
+    *p = SPLIT ? make_float4(a[0], a[1], a[2], a[3]) : make_float4(a[0], b[0], a[1], b[1]);
+    *q = SPLIT ? make_float4(b[0], b[1], b[2], b[3]) : make_float4(a[2], b[2], a[3], b[3]);
+  } else if constexpr (SPLIT) {
+    *reinterpret_cast<uint2*>(row + 4 * l) = make_uint2(pack2(a[0], a[1], T()), pack2(a[2], a[3], T()));
+    *reinterpret_cast<uint2*>(row + D / 2 + 4 * l) = make_uint2(pack2(b[0], b[1], T()), pack2(b[2], b[3], T()));
   } else {
-    *reinterpret_cast<uint4*>(row + 8 * l) = make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()),
-                                                        pack2(f[4], f[5], T()), pack2(f[6], f[7], T()));
+    *reinterpret_cast<uint4*>(row + 8 * l) = make_uint4(pack2(a[0], b[0], T()), pack2(a[1], b[1], T()),
+                                                        pack2(a[2], b[2], T()), pack2(a[3], b[3], T()));
   }
 }
 
@@ -192,12 +214,12 @@ __device__ __forceinline__ void lane_angles(const RopeDev& r, const LanePairs& l
       }
     }
   } else if (n < r.ngrid) {
-    const int i = static_cast<int>(n);              // the grid has fewer than 2^31 tokens
-    const int row = i / r.gw;
-    p[2] = r.first[2] + (i - row * r.gw);
-    const int fr = row / r.gh;
-    p[1] = r.first[1] + (row - fr * r.gh);
-    p[0] = r.first[0] + fr;
+    const uint32_t i = static_cast<uint32_t>(n);    // the grid has fewer than 2^31 tokens
+    const uint32_t row = static_cast<uint32_t>((static_cast<uint64_t>(i) * r.mw) >> r.sw);
+    const uint32_t fr = static_cast<uint32_t>((static_cast<uint64_t>(row) * r.mh) >> r.sh);
+    p[2] = r.first[2] + static_cast<int>(i - row * r.gw);
+    p[1] = r.first[1] + static_cast<int>(row - fr * r.gh);
+    p[0] = r.first[0] + static_cast<int>(fr);
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -212,32 +234,24 @@ __device__ __forceinline__ void lane_angles(const RopeDev& r, const LanePairs& l
   }
 }
 
-// Pairs of a row turned in place.  A pair with sin = 0 leaves its members
-// apart, so that an unturned pair is a copy even next to an infinity.
-__device__ __forceinline__ void turn(float (&f)[8], const float (&c)[4], const float (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = f[2 * i], b = f[2 * i + 1];
-    const bool on = s[i] != 0.f;
-    f[2 * i] = on ? a * c[i] - b * s[i] : a * c[i];
-    f[2 * i + 1] = on ? a * s[i] + b * c[i] : b * c[i];
-  }
-}
+// (x, y) = (u c + v s, w c + z s) forms below are fused multiply-adds in packed
+// pairs: -v for a subtraction is a sign flip of both halves.
+__device__ __forceinline__ uint64_t f2neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
 
 template <bool SPLIT, int D, typename T>
-__device__ __forceinline__ void lane_weight(const void* w, int w_f32, int l, float (&f)[8]) {
+__device__ __forceinline__ Row8 lane_weight(const void* w, int w_f32, int l) {
   if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-  } else if (w_f32) {
+    const uint64_t one = f2pack(1.f, 1.f);
+    return Row8{{one, one}, {one, one}};
+  }
+  if (w_f32) {
     Vec8<float> v;
     load8<SPLIT, D>(static_cast<const float*>(w), l, v);
-    to_pairs<SPLIT>(v, f);
-  } else {
-    Vec8<T> v;
-    load8<SPLIT, D>(static_cast<const T*>(w), l, v);
-    to_pairs<SPLIT>(v, f);
+    return to_row<SPLIT>(v);
   }
+  Vec8<T> v;
+  load8<SPLIT, D>(static_cast<const T*>(w), l, v);
+  return to_row<SPLIT>(v);
 }
 
 template <int D>
@@ -246,55 +260,96 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = D / 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+__device__ __forceinline__ float f2sum(uint64_t v) {
+  float a, b;
+  f2unpack(v, a, b);
+  return a + b;
+}
 
-// Forward: rotation, with the norm before it when NORM.
+// Forward: rotation, with the norm before it when NORM.  Grid (blocks over the
+// tokens, tensors, parts of the heads).
 template <typename T, int D, bool SPLIT, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 8;                            // lanes per row
+  constexpr int kGroups = kRopeThreads / G;
   const RopeTensor& t = p.t[blockIdx.y];
+  const int h0 = blockIdx.z * p.per, heads = min(p.per, t.H - h0);
+  if (heads <= 0) return;
   const int l = threadIdx.x % G;
   LanePairs lp;
   lane_pairs(p.r, l, lp);
-  float w[8];
-  if (NORM) lane_weight<SPLIT, D, T>(t.w, p.w_f32, l, w);
-  const long long items = p.N * t.chunks;
-  constexpr int kGroups = kRopeThreads / G;
+  Row8 w;
+  if (NORM) w = lane_weight<SPLIT, D, T>(t.w, p.w_f32, l);
   // every lane of a warp runs the same number of steps (the butterflies take
-  // the whole warp); groups past the end work on no head
-  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < items;
+  // the whole warp); groups past the last token load and store nothing
+  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < p.N;
        base += static_cast<long long>(gridDim.x) * kGroups) {
-    const long long it = base + threadIdx.x / G;
-    const long long n = it / t.chunks;
-    const int h0 = static_cast<int>(it - n * t.chunks) * t.per;
-    const int nh = it < items ? min(t.per, t.H - h0) : 0;
+    const long long n = base + threadIdx.x / G;
+    const bool on = n < p.N;
     const T* x = static_cast<const T*>(t.x) + n * t.xt + h0 * t.xh;
     T* y = static_cast<T*>(t.y) + n * t.yt + h0 * t.yh;
-    Vec8<T> v[kRopeHeads];
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (on) lane_angles(p.r, lp, n, c, s);
+    // y_a = a ca + b sb, y_b = a sa + b cb, with the weights of a and b inside
+    uint64_t ca[2], sb[2], sa[2], cb[2];
 #pragma unroll
-    for (int u = 0; u < kRopeHeads; ++u)
-      if (u < nh) load8<SPLIT, D>(x + u * t.xh, l, v[u]);
-    float c[4], s[4];
-    if (nh > 0) lane_angles(p.r, lp, n, c, s);
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t cc = f2pack(c[2 * i], c[2 * i + 1]), ss = f2pack(s[2 * i], s[2 * i + 1]);
+      ca[i] = NORM ? fmul2(cc, w.a[i]) : cc;
+      cb[i] = NORM ? fmul2(cc, w.b[i]) : cc;
+      sa[i] = NORM ? fmul2(ss, w.a[i]) : ss;
+      sb[i] = f2neg(NORM ? fmul2(ss, w.b[i]) : ss);
+    }
+    // an unturned pair is a copy, even next to an infinity
+    const bool turned = s[0] != 0.f && s[1] != 0.f && s[2] != 0.f && s[3] != 0.f;
+#pragma unroll 1
+    for (int b = 0; b < heads; b += kRopeHeads) {
+      Vec8<T> v[kRopeHeads];
 #pragma unroll
-    for (int u = 0; u < kRopeHeads; ++u) {
-      if (NORM) {
-        if (u >= t.per) break;                        // the same for the whole grid
-      } else if (u >= nh) {
-        break;
+      for (int u = 0; u < kRopeHeads; ++u)
+        if (on && b + u < heads) load8<SPLIT, D>(x + (b + u) * t.xh, l, v[u]);
+#pragma unroll
+      for (int u = 0; u < kRopeHeads; ++u) {
+        if (b + u >= heads) break;                    // the same for the whole block
+        const Row8 f = to_row<SPLIT>(v[u]);
+        Row8 o;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          o.a[i] = ffma2(f.b[i], sb[i], fmul2(f.a[i], ca[i]));
+          o.b[i] = ffma2(f.a[i], sa[i], fmul2(f.b[i], cb[i]));
+        }
+        if (NORM) {
+          const uint64_t q = ffma2(f.b[1], f.b[1], ffma2(f.a[1], f.a[1], ffma2(f.b[0], f.b[0], fmul2(f.a[0], f.a[0]))));
+          const float ss = group_sum<D>(f2sum(q));
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          const uint64_t rr = f2pack(r, r);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o.a[i] = fmul2(o.a[i], rr);
+            o.b[i] = fmul2(o.b[i], rr);
+          }
+        } else if (!turned) {
+          float a[4], e[4], oa[4], oe[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f2unpack(f.a[i], a[2 * i], a[2 * i + 1]);
+            f2unpack(f.b[i], e[2 * i], e[2 * i + 1]);
+            f2unpack(o.a[i], oa[2 * i], oa[2 * i + 1]);
+            f2unpack(o.b[i], oe[2 * i], oe[2 * i + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            oa[i] = s[i] != 0.f ? oa[i] : a[i] * c[i];
+            oe[i] = s[i] != 0.f ? oe[i] : e[i] * c[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o.a[i] = f2pack(oa[2 * i], oa[2 * i + 1]);
+            o.b[i] = f2pack(oe[2 * i], oe[2 * i + 1]);
+          }
+        }
+        if (on) store8<SPLIT, D>(y + (b + u) * t.yh, l, o);
       }
-      float f[8];
-      to_pairs<SPLIT>(v[u], f);
-      if (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        ss = group_sum<D>(ss);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
-      }
-      turn(f, c, s);
-      if (u < nh) store8<SPLIT, D>(y + u * t.yh, l, f);
     }
   }
 }
@@ -304,84 +359,82 @@ __global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const __grid_con
 // rope_dw_kernel adds the blocks' partial sums, again in a fixed order, so
 // that the result does not change from run to run.
 template <typename T, int D, bool SPLIT>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 8;
   constexpr int kGroups = kRopeThreads / G;
-  __shared__ float s_dw[kGroups][D];
+  __shared__ __align__(16) float s_dw[kGroups][D];
   const RopeTensor& t = p.t[blockIdx.y];
+  const int h0 = blockIdx.z * p.per, heads = min(p.per, t.H - h0);
   const int l = threadIdx.x % G;
   LanePairs lp;
   lane_pairs(p.r, l, lp);
-  float w[8], dw[8];
-  lane_weight<SPLIT, D, T>(t.w, p.w_f32, l, w);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-  const long long items = p.N * t.chunks;
-  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < items;
+  const Row8 w = lane_weight<SPLIT, D, T>(t.w, p.w_f32, l);
+  const uint64_t zero = f2pack(0.f, 0.f);
+  Row8 dw{{zero, zero}, {zero, zero}};
+  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < p.N;
        base += static_cast<long long>(gridDim.x) * kGroups) {
-    const long long it = base + threadIdx.x / G;
-    const long long n = it / t.chunks;
-    const int h0 = static_cast<int>(it - n * t.chunks) * t.per;
-    const int nh = it < items ? min(t.per, t.H - h0) : 0;
+    const long long n = base + threadIdx.x / G;
+    const bool on = n < p.N;
     const T* x = static_cast<const T*>(t.x) + n * t.xt + h0 * t.xh;
     const T* g = static_cast<const T*>(t.g) + n * t.gt + h0 * t.gh;
     T* y = static_cast<T*>(t.y) + n * t.yt + h0 * t.yh;
-    float c[4], s[4];
-    bool have = false;
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (on) lane_angles(p.r, lp, n, c, s);            // s: of the angle turned back
+    const uint64_t cc[2] = {f2pack(c[0], c[1]), f2pack(c[2], c[3])};
+    const uint64_t ss[2] = {f2pack(s[0], s[1]), f2pack(s[2], s[3])};
 #pragma unroll 1
-    for (int b = 0; b < t.per; b += 4) {              // four heads' loads in flight
-      Vec8<T> vx[4], vg[4];
+    for (int b = 0; b < heads; b += kRopeHeads) {
+      Vec8<T> vx[kRopeHeads], vg[kRopeHeads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (b + u < nh) {
+      for (int u = 0; u < kRopeHeads; ++u) {
+        if (on && b + u < heads) {
           load8<SPLIT, D>(x + (b + u) * t.xh, l, vx[u]);
           load8<SPLIT, D>(g + (b + u) * t.gh, l, vg[u]);
         }
       }
-      if (!have && nh > 0) lane_angles(p.r, lp, n, c, s);
-      have = true;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (b + u >= t.per) break;                    // the same for the whole grid
-        float fx[8], fg[8];
-        to_pairs<SPLIT>(vx[u], fx);
-        to_pairs<SPLIT>(vg[u], fg);
-        float ss = 0.f, dot = 0.f;
-        turn(fg, c, s);                               // back: the sign is in s
+      for (int u = 0; u < kRopeHeads; ++u) {
+        if (b + u >= heads) break;                    // the same for the whole block
+        const Row8 fx = to_row<SPLIT>(vx[u]), fg = to_row<SPLIT>(vg[u]);
+        Row8 z, zx;                                   // g turned back, and times x
+        uint64_t q = zero, dot = zero;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(fx[i], fx[i], ss);
-          dot = fmaf(fg[i] * w[i], fx[i], dot);
+        for (int i = 0; i < 2; ++i) {
+          z.a[i] = ffma2(f2neg(fg.b[i]), ss[i], fmul2(fg.a[i], cc[i]));
+          z.b[i] = ffma2(fg.a[i], ss[i], fmul2(fg.b[i], cc[i]));
+          zx.a[i] = fmul2(z.a[i], fx.a[i]);
+          zx.b[i] = fmul2(z.b[i], fx.b[i]);
+          q = ffma2(fx.b[i], fx.b[i], ffma2(fx.a[i], fx.a[i], q));
+          dot = ffma2(zx.b[i], w.b[i], ffma2(zx.a[i], w.a[i], dot));
         }
-        ss = group_sum<D>(ss);
-        dot = group_sum<D>(dot);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = dot * r * (1.f / D);          // mean(g w xh)
-        if (b + u < nh) {
-          float f[8];
+        const float sq = group_sum<D>(f2sum(q));
+        const float sd = group_sum<D>(f2sum(dot));
+        const float r = rsqrtf(sq * (1.f / D) + p.eps);
+        const float m = -(sd * r) * (1.f / D) * r * r;   // -mean(g w xh) r^2: dx = r g w + x m
+        const uint64_t rr = f2pack(r, r), mm = f2pack(m, m);
+        if (on) {
+          Row8 o;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float xh = fx[i] * r;
-            dw[i] = fmaf(fg[i], xh, dw[i]);
-            f[i] = r * (fg[i] * w[i] - xh * m);
+          for (int i = 0; i < 2; ++i) {
+            dw.a[i] = ffma2(zx.a[i], rr, dw.a[i]);
+            dw.b[i] = ffma2(zx.b[i], rr, dw.b[i]);
+            o.a[i] = ffma2(fx.a[i], mm, fmul2(fmul2(z.a[i], w.a[i]), rr));
+            o.b[i] = ffma2(fx.b[i], mm, fmul2(fmul2(z.b[i], w.b[i]), rr));
           }
-          store8<SPLIT, D>(y + (b + u) * t.yh, l, f);
+          store8<SPLIT, D>(y + (b + u) * t.yh, l, o);
         }
       }
     }
   }
-  // channel of dw[i]: the inverse of the pair order
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s_dw[threadIdx.x / G][SPLIT ? 4 * l + i : 8 * l + 2 * i] = dw[2 * i];
-    s_dw[threadIdx.x / G][SPLIT ? D / 2 + 4 * l + i : 8 * l + 2 * i + 1] = dw[2 * i + 1];
-  }
+  // channels of the pairs
+  store8<SPLIT, D>(s_dw[threadIdx.x / G], l, dw);
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) sum += s_dw[gr][threadIdx.x];
-    p.partial[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * D + threadIdx.x] = sum;
+    const size_t block = (static_cast<size_t>(blockIdx.y) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x;
+    p.partial[block * D + threadIdx.x] = sum;
   }
 }
 

@@ -57,8 +57,8 @@ struct PoolSmem {
 // stride over the tiles, slabs of the same tokens first.  One warp keeps
 // kPoolStages boxes in flight (with three blocks an SM 144 KB, against the 43 KB
 // that the memory's latency asks for), so that the loads do not wait for the
-// adds: with loads and adds in the same warps the pass read 4.4 TB/s, this way
-// NEW TB/s.
+// adds: with loads and adds in the same warps the pass read 4.2 TB/s, this way
+// 5.0 TB/s (ncu, 196560 x 12 x 128).
 //
 // The other warps add 4 tokens of each box, 8 channels a lane, in 64 bits in
 // order, then the eight warps' sums in order: bf16 values are 8 bits wide, so

@@ -490,6 +490,19 @@ extern "C" int blocksparse_attn_fwd_noalloc(const void* q, const void* k, const 
 // Rotary positions and the normed rotation of queries and keys.
 namespace {
 
+// per-device opt-in to large dynamic shared memory, set once per kernel
+template <typename K>
+int allow_smem(K* kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BSA_ERR_CUDA;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return BSA_ERR_CUDA;
+    done[dev].store(true, std::memory_order_release);
+  }
+  return BSA_OK;
+}
+
 int esize(int dtype) { return dtype == BSA_F32 ? 4 : 2; }
 
 // rows of an output tensor must not overlap
@@ -586,8 +599,8 @@ void set_tensor(RopeTensor* t, const bsa_heads* x, const bsa_heads* g, const bsa
   t->w = w;
 }
 
-// Grid of a rotation: blocks over the tokens (at most `most` in all, each then
-// strides), tensors, parts of the heads.  A block takes all heads of its tokens,
+// Grid of a rotation: blocks over the tokens (at most `most` in all, as many as
+// are resident; each strides), tensors, parts of the heads.  A block takes all heads of its tokens,
 // so that their angles are looked up once; with too few tokens to fill the
 // SMs the heads are dealt to several blocks, kRopeHeads at the least.
 dim3 rope_grid(RopeParams* p, int tensors, int d, long long most) {
@@ -605,17 +618,17 @@ dim3 rope_grid(RopeParams* p, int tensors, int d, long long most) {
   return dim3(static_cast<unsigned>(x), tensors, parts);
 }
 
+template <typename T, int D, bool SPLIT, bool NORM>
+int launch_rope_fwd(RopeParams& p, int tensors, cudaStream_t st) {
+  const dim3 grid = rope_grid(&p, tensors, D, 148 * kRopeFwdCtas);
+  rope_fwd_kernel<T, D, SPLIT, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 template <typename T, int D>
 int launch_rope_fwd(RopeParams& p, int tensors, bool split, bool norm, cudaStream_t st) {
-  const dim3 grid = rope_grid(&p, tensors, D, 148 * 3 * 4);
-  if (split) {
-    if (norm) rope_fwd_kernel<T, D, true, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else rope_fwd_kernel<T, D, true, false><<<grid, kRopeThreads, 0, st>>>(p);
-  } else {
-    if (norm) rope_fwd_kernel<T, D, false, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else rope_fwd_kernel<T, D, false, false><<<grid, kRopeThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  if (split) return norm ? launch_rope_fwd<T, D, true, true>(p, tensors, st) : launch_rope_fwd<T, D, true, false>(p, tensors, st);
+  return norm ? launch_rope_fwd<T, D, false, true>(p, tensors, st) : launch_rope_fwd<T, D, false, false>(p, tensors, st);
 }
 
 int launch_rope_fwd_any(RopeParams& p, int dtype, int d, int tensors, bool split, bool norm, cudaStream_t st) {
@@ -631,13 +644,20 @@ int launch_rope_fwd_any(RopeParams& p, int dtype, int d, int tensors, bool split
 
 // most blocks of the backward pass (all tensors and parts of the heads): their
 // weight-gradient partial sums are added by one block per tensor afterwards
-constexpr long long kRopeBwdBlocks = 148 * 4;
+constexpr long long kRopeBwdBlocks = 148 * kRopeBwdCtas;
+
+template <typename T, int D, bool SPLIT>
+int launch_rope_bwd(const RopeParams& p, dim3 grid, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  const int rc = allow_smem(rope_bwd_kernel<T, D, SPLIT>, kRopeRing, done);
+  if (rc != BSA_OK) return rc;
+  rope_bwd_kernel<T, D, SPLIT><<<grid, kRopeThreads, kRopeRing, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
 
 template <typename T, int D>
 int launch_rope_bwd(const RopeParams& p, bool split, dim3 grid, cudaStream_t st) {
-  if (split) rope_bwd_kernel<T, D, true><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_bwd_kernel<T, D, false><<<grid, kRopeThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  return split ? launch_rope_bwd<T, D, true>(p, grid, st) : launch_rope_bwd<T, D, false>(p, grid, st);
 }
 
 int launch_rope_bwd_any(const RopeParams& p, int dtype, int d, bool split, dim3 grid, cudaStream_t st) {
@@ -770,19 +790,6 @@ int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* 
 // ---------------------------------------------------------------------------
 // Key blocks by block means.
 namespace {
-
-// per-device opt-in to large dynamic shared memory, set once per kernel
-template <typename K>
-int allow_smem(K* kernel, int bytes, std::atomic<bool>* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BSA_ERR_CUDA;
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-      return BSA_ERR_CUDA;
-    done[dev].store(true, std::memory_order_release);
-  }
-  return BSA_OK;
-}
 
 // Workspace: means (64-bit), norms, the two bf16 parts, rough scores of the
 // heads of one pass.

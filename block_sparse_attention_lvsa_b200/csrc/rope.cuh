@@ -20,20 +20,32 @@
 // neighbouring lanes own one row, four pairs (eight channels) a lane, so both
 // members of a pair, the table entries and the weights of a lane's channels
 // stay in that lane; the row sums are butterflies over d/8 lanes.  A group of
-// d/8 lanes goes through the heads of one token, kRopeHeads rows' loads at a
-// time, with the token's cos and sin (times the weights) in registers, and the
-// blocks stride over the tokens, so that a lane finds its pairs once.  The
-// arithmetic is in packed pairs of float32 (half the instructions: with scalar
-// ones and one token and eight heads a block the kernel was bound by
-// instruction issue, NEW1); the one rounding is the store.
+// d/8 lanes goes through the heads of one token, four rows' loads at a time,
+// with the token's cos and sin (times the weights) in registers, and the blocks
+// stride over the tokens, so that a lane finds its pairs once.  The arithmetic
+// is in packed pairs of float32 (half the instructions: with scalar ones, and
+// the angles looked up again for every eight heads, the kernel was bound by
+// instruction issue); the one rounding is the store.  One B200, bf16, q and k of
+// 196560 x 12 x 128 (2.42 GB): 400 us, 0.92 of the measured copy bandwidth
+// (first form 571 us); the rotation alone of one of them 191 us, 0.96.
+// The backward pass has three streams and more to compute per row; its loads go
+// through a ring in shared memory, two steps ahead: 340 us at 32760 x 40 x 128,
+// 0.90 (loads in registers 415 us; the forward pass is slower with a ring, 437
+// against 391 us).
 #pragma once
 #include <cuda_fp16.h>
 #include "attn_fwd.cuh"
 
 namespace bsa {
 
-constexpr int kRopeHeads = 4;        // rows of a group whose loads are in flight
+constexpr int kRopeHeads = 4;        // rows of a group per step (32-bit types: half)
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBwdStages = 3;    // steps of the backward kernel's load ring
+constexpr int kRopeFwdCtas = 3, kRopeBwdCtas = 2;          // blocks per SM
+template <typename T>
+constexpr int rope_rows() { return sizeof(T) == 4 ? kRopeHeads / 2 : kRopeHeads; }
+// ring bytes: 16 (32) bytes a lane of every row of x and g
+constexpr int kRopeRing = kRopeBwdStages * 2 * kRopeHeads * 16 * kRopeThreads;
 
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -83,6 +95,51 @@ template <typename T> struct Vec8 {
 template <> struct Vec8<float> {
   float4 a, b;
 };
+
+// Ring in shared memory: every lane copies its channels of the next rows
+// asynchronously into a slot of its own (so that nobody else waits for them)
+// and reads them back two steps later.  `slot` is the lane's slot of a row; a
+// row of 32-bit values takes a second one behind all lanes'.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+constexpr uint32_t kRopeSlots = 16 * kRopeThreads;
+template <bool SPLIT, int D, typename T>
+__device__ __forceinline__ void copy8(uint32_t slot, const T* row, int l) {
+  if constexpr (sizeof(T) == 4) {
+    cp_async16(slot, row + (SPLIT ? 4 * l : 8 * l));
+    cp_async16(slot + kRopeSlots, row + (SPLIT ? D / 2 + 4 * l : 8 * l + 4));
+  } else if constexpr (SPLIT) {
+    cp_async8(slot, row + 4 * l);
+    cp_async8(slot + 8, row + D / 2 + 4 * l);
+  } else {
+    cp_async16(slot, row + 8 * l);
+  }
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void read8(uint32_t slot, Vec8<float>& v) {
+  const uint4 a = ld_shared_u4(slot), b = ld_shared_u4(slot + kRopeSlots);
+  v.a = make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w));
+  v.b = make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w));
+}
+template <typename T>
+__device__ __forceinline__ void read8(uint32_t slot, Vec8<T>& v) {
+  const uint4 a = ld_shared_u4(slot);
+  v.a = make_uint2(a.x, a.y);
+  v.b = make_uint2(a.z, a.w);
+}
 // The same as packed pairs of float: members a of pairs (0, 1) and (2, 3),
 // members b of the same pairs.
 struct Row8 {
@@ -269,9 +326,9 @@ __device__ __forceinline__ float f2sum(uint64_t v) {
 // Forward: rotation, with the norm before it when NORM.  Grid (blocks over the
 // tokens, tensors, parts of the heads).
 template <typename T, int D, bool SPLIT, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeFwdCtas) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 8;                            // lanes per row
-  constexpr int kGroups = kRopeThreads / G;
+  constexpr int kGroups = kRopeThreads / G, kRows = rope_rows<T>();
   const RopeTensor& t = p.t[blockIdx.y];
   const int h0 = blockIdx.z * p.per, heads = min(p.per, t.H - h0);
   if (heads <= 0) return;
@@ -303,13 +360,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_fwd_kernel(const __grid_
     // an unturned pair is a copy, even next to an infinity
     const bool turned = s[0] != 0.f && s[1] != 0.f && s[2] != 0.f && s[3] != 0.f;
 #pragma unroll 1
-    for (int b = 0; b < heads; b += kRopeHeads) {
-      Vec8<T> v[kRopeHeads];
+    for (int b = 0; b < heads; b += kRows) {
+      Vec8<T> v[kRows];
 #pragma unroll
-      for (int u = 0; u < kRopeHeads; ++u)
+      for (int u = 0; u < kRows; ++u)
         if (on && b + u < heads) load8<SPLIT, D>(x + (b + u) * t.xh, l, v[u]);
 #pragma unroll
-      for (int u = 0; u < kRopeHeads; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         if (b + u >= heads) break;                    // the same for the whole block
         const Row8 f = to_row<SPLIT>(v[u]);
         Row8 o;
@@ -359,43 +416,66 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_fwd_kernel(const __grid_
 // rope_dw_kernel adds the blocks' partial sums, again in a fixed order, so
 // that the result does not change from run to run.
 template <typename T, int D, bool SPLIT>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 8;
-  constexpr int kGroups = kRopeThreads / G;
+  constexpr int kGroups = kRopeThreads / G, kRows = rope_rows<T>(), kStages = kRopeBwdStages;
+  constexpr uint32_t kRow = sizeof(T) == 4 ? 2 * kRopeSlots : kRopeSlots, kStage = 2 * kRows * kRow;   // x, g
+  extern __shared__ __align__(128) uint8_t smem_rope[];
   __shared__ __align__(16) float s_dw[kGroups][D];
   const RopeTensor& t = p.t[blockIdx.y];
   const int h0 = blockIdx.z * p.per, heads = min(p.per, t.H - h0);
   const int l = threadIdx.x % G;
+  const uint32_t slot = smem_u32(smem_rope) + threadIdx.x * 16;
+  const long long first = static_cast<long long>(blockIdx.x) * kGroups, stride = static_cast<long long>(gridDim.x) * kGroups;
+  long long ahead = first;
+  int ahead_b = 0;
+  const T* xa = static_cast<const T*>(t.x) + (first + threadIdx.x / G) * t.xt + h0 * t.xh;
+  const T* ga = static_cast<const T*>(t.g) + (first + threadIdx.x / G) * t.gt + h0 * t.gh;
+  auto load = [&](int stage) {
+    if (ahead + threadIdx.x / G < p.N) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (ahead_b + u < heads) {
+          copy8<SPLIT, D>(slot + stage * kStage + 2 * u * kRow, xa + (ahead_b + u) * t.xh, l);
+          copy8<SPLIT, D>(slot + stage * kStage + (2 * u + 1) * kRow, ga + (ahead_b + u) * t.gh, l);
+        }
+      }
+    }
+    cp_async_commit();
+    ahead_b += kRows;
+    if (ahead_b >= heads) {
+      ahead_b = 0;
+      ahead += stride;
+      xa += stride * t.xt;
+      ga += stride * t.gt;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i);
   LanePairs lp;
   lane_pairs(p.r, l, lp);
   const Row8 w = lane_weight<SPLIT, D, T>(t.w, p.w_f32, l);
   const uint64_t zero = f2pack(0.f, 0.f);
   Row8 dw{{zero, zero}, {zero, zero}};
-  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < p.N;
-       base += static_cast<long long>(gridDim.x) * kGroups) {
+  int stage = 0;
+  for (long long base = first; base < p.N; base += stride) {
     const long long n = base + threadIdx.x / G;
     const bool on = n < p.N;
-    const T* x = static_cast<const T*>(t.x) + n * t.xt + h0 * t.xh;
-    const T* g = static_cast<const T*>(t.g) + n * t.gt + h0 * t.gh;
     T* y = static_cast<T*>(t.y) + n * t.yt + h0 * t.yh;
     float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
     if (on) lane_angles(p.r, lp, n, c, s);            // s: of the angle turned back
     const uint64_t cc[2] = {f2pack(c[0], c[1]), f2pack(c[2], c[3])};
     const uint64_t ss[2] = {f2pack(s[0], s[1]), f2pack(s[2], s[3])};
 #pragma unroll 1
-    for (int b = 0; b < heads; b += kRopeHeads) {
-      Vec8<T> vx[kRopeHeads], vg[kRopeHeads];
+    for (int b = 0; b < heads; b += kRows) {
+      cp_async_wait<kStages - 2>();
 #pragma unroll
-      for (int u = 0; u < kRopeHeads; ++u) {
-        if (on && b + u < heads) {
-          load8<SPLIT, D>(x + (b + u) * t.xh, l, vx[u]);
-          load8<SPLIT, D>(g + (b + u) * t.gh, l, vg[u]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeHeads; ++u) {
+      for (int u = 0; u < kRows; ++u) {
         if (b + u >= heads) break;                    // the same for the whole block
-        const Row8 fx = to_row<SPLIT>(vx[u]), fg = to_row<SPLIT>(vg[u]);
+        Vec8<T> vx, vg;
+        read8(slot + stage * kStage + 2 * u * kRow, vx);
+        read8(slot + stage * kStage + (2 * u + 1) * kRow, vg);
+        const Row8 fx = to_row<SPLIT>(vx), fg = to_row<SPLIT>(vg);
         Row8 z, zx;                                   // g turned back, and times x
         uint64_t q = zero, dot = zero;
 #pragma unroll
@@ -424,8 +504,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
           store8<SPLIT, D>(y + (b + u) * t.yh, l, o);
         }
       }
+      load(stage == 0 ? kStages - 1 : stage - 1);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
   }
+  cp_async_wait<0>();
   // channels of the pairs
   store8<SPLIT, D>(s_dw[threadIdx.x / G], l, dw);
   __syncthreads();

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -410,7 +411,7 @@ def losa_select(mass: torch.Tensor, tau: float = 0.99, idx=None, cnt=None, strea
 # ------------------------------------------- rotary positions, normed q and k ---
 _DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16, torch.float32: BSA_F32}
 _PAIRINGS = {"adjacent": BSA_ROPE_ADJACENT, "split": BSA_ROPE_SPLIT}
-_I3, _P3 = ctypes.c_int * 3, ctypes.c_void_p * 3
+_ROPE = struct.Struct("@i3i3i3P3i3iP")         # bsa_rope, packed in one go
 _raw_stream = torch._C._cuda_getCurrentRawStream       # handle of a device's current stream, without a Stream object
 
 
@@ -536,7 +537,7 @@ def rope_axes(tables, grid=None, first=(0, 0, 0), pos: Optional[torch.Tensor] = 
     if (grid is None) == (pos is None):
         raise ValueError("give either grid or pos")
     dev = None
-    pairs, lens, ptrs = [0, 0, 0], [0, 0, 0], [None, None, None]
+    pairs, lens, ptrs = [0, 0, 0], [0, 0, 0], [0, 0, 0]
     for a, t in enumerate(tables):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 3 or not t.is_cuda or \
                 t.shape[2] != 2 or not t.is_contiguous():
@@ -555,8 +556,11 @@ def rope_axes(tables, grid=None, first=(0, 0, 0), pos: Optional[torch.Tensor] = 
         if len(grid) != n or len(first) < n:
             raise ValueError("grid and first must give every axis")
         g, f = grid + (1,) * (3 - n), first[:n] + (0,) * (3 - n)
-    r = bsa_rope(_PAIRINGS[pairing], _I3(*pairs), _I3(*lens), _P3(*ptrs), _I3(*g), _I3(*f),
-                 None if pos is None else pos.data_ptr())
+    try:
+        r = bsa_rope.from_buffer_copy(_ROPE.pack(_PAIRINGS[pairing], *pairs, *lens, *ptrs, *g, *f,
+                                                 0 if pos is None else pos.data_ptr()))
+    except struct.error as e:
+        raise ValueError(f"grid and first must be whole numbers of 32 bits, got {grid} and {first}") from e
     r._device, r._pos = dev, pos
     r._tensors = (tuple(tables), pos)      # the struct holds raw pointers: keep the tensors alive with it
     return r

@@ -26,7 +26,7 @@
 //     hold (32-bit products near the ends of the exponent, values that are not
 //     finite) get 64-bit scores throughout.
 #pragma once
-#include "ptx.cuh"
+#include "rope.cuh"   // packed pairs of float
 
 namespace bsa {
 
@@ -35,14 +35,6 @@ constexpr int kPoolWarps = 8;                          // adding warps; one more
 constexpr int kPoolThreads = 32 * (kPoolWarps + 1);
 constexpr int kPoolStages = 3;                         // 32 tokens x 256 channels each
 constexpr int kPoolCtas = 3;                           // per SM
-
-// A finite bf16 times 2^-896 as a 64-bit float, by moving its bits: the sign,
-// and the exponent and significand 3 places down; the exponent then counts from
-// 1023 instead of 127, and zero and subnormals stay what they are.  `w`: the
-// bf16 in the upper half of a word, anything in the lower.
-__device__ __forceinline__ double moved(uint32_t w) {
-  return __hiloint2double(static_cast<int>((static_cast<int32_t>(w) >> 3) & 0x8FFFE000), 0);
-}
 
 struct PoolSmem {
   static constexpr uint32_t kStage = 32 * 512;
@@ -57,16 +49,14 @@ struct PoolSmem {
 // stride over the tiles, slabs of the same tokens first.  One warp keeps
 // kPoolStages boxes in flight (with three blocks an SM 144 KB, against the 43 KB
 // that the memory's latency asks for), so that the loads do not wait for the
-// adds: with loads and adds in the same warps the pass read 4.2 TB/s, this way
-// 5.0 TB/s (ncu, 196560 x 12 x 128).
-//
-// The other warps add 4 tokens of each box, 8 channels a lane, in 64 bits in
-// order, then the eight warps' sums in order: bf16 values are 8 bits wide, so
+// adds.  The other warps add 4 tokens of each box, 8 channels a lane, in 64 bits
+// in order, then the eight warps' sums in order: bf16 values are 8 bits wide, so
 // such a sum is exact unless the block spans more than 2^38, and equal blocks
-// always give equal means.  Half of the values become 64-bit by the conversion
-// instruction, half by `moved`: each way alone holds its own pipe longer than
-// the loads take.  A channel that may hold a value that is not finite (its
-// 32-bit sum is not) is added again with the conversion.
+// always give equal means.
+// 225 us under ncu for q and k of 196560 x 12 x 128 (1.21 GB, 5.4 TB/s); the unit
+// that converts to 64 bits is 69% busy.  Loads and adds in the same warps: 272 us;
+// half of the conversions by moving bits in the integer pipe: 246 us; four
+// adding warps with twice the tokens each: 285 us.
 // mean: [2][H][nB][d] double; hi, lo: bf16 [2][H][nB][d]; norm: [2][H][nB] double.
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -115,22 +105,19 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel
     return;
   }
 
-  int it = 0;
+  int slot = 0;
+  uint32_t phase = 0;
   bool ok = true;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int slab = static_cast<int>(t % slabs);
     const int zb = static_cast<int>(t / slabs), z = zb >= nB, b = zb - z * nB;
     const int rows = min(128, N - b * 128);
     double acc[8];                                    // odd channels times 2^-896
-    float rough[4];                                   // 32-bit sums of the odd channels
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rough[i] = 0.f;
 #pragma unroll 1
-    for (int u = 0; u < 4; ++u, ++it) {
-      const int slot = it % kPoolStages;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(slot), (it / kPoolStages) & 1, limit));
+    for (int u = 0; u < 4; ++u) {
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full(slot), phase, limit));
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -143,23 +130,12 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           acc[2 * c] += static_cast<double>(__uint_as_float(w[c] << 16));
-          acc[2 * c + 1] += moved(w[c]);
-          rough[c] += __uint_as_float(w[c]);
+          acc[2 * c + 1] += static_cast<double>(__uint_as_float(w[c] & 0xFFFF0000u));
         }
       }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[2 * c + 1] *= 0x1p+896;
-      if (!isfinite(rough[c])) {
-        const int ch = slab * 256 + lane * 8 + 2 * c + 1;
-        const __nv_bfloat16* x = z ? k : q;
-        double s = 0.0;
-        for (int i = 0; ch < row && i < 16; ++i) {
-          const int tok = (i >> 2) * 32 + warp * 4 + (i & 3);
-          if (tok < rows) s += static_cast<double>(__bfloat162float(x[(static_cast<size_t>(b) * 128 + tok) * row + ch]));
-        }
-        acc[2 * c + 1] = s;
+      if (++slot == kPoolStages) {
+        slot = 0;
+        phase ^= 1;
       }
     }
 #pragma unroll
@@ -205,7 +181,9 @@ struct ScoreSmem {
   static constexpr uint32_t kAlloc = kHolder + 16 + 1024;
 };
 
-// Rough scores of 128 query blocks x 128 key blocks of one head.  hi and lo
+// Rough scores of 128 query blocks x 128 key blocks of one head: 58 us for 12 heads
+// of 1536 x 1536 at d = 128 (21.7 GFLOP in three products; loading four tiles and
+// writing one is the larger part of a block's 5 us).  hi and lo
 // are mapped (d, nB, 2 H): heads of q, then heads of k; scores (nB, nB, heads).
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads)
@@ -310,6 +288,11 @@ __device__ __forceinline__ float warp_max_f(float v) {
 // warps (rows) per block; four long rows fill shared memory
 __host__ __device__ constexpr int sel_warps(int c4) { return c4 ? 8 : 4; }
 constexpr int kSelKeys = 32;
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
 constexpr float kRoughError = 1.0f / 8192.0f;         // E / (|q| max |k|), see above
 
 // One warp per row (grid (groups of rows, heads of the pass)).  Block j sits
@@ -319,7 +302,8 @@ constexpr float kRoughError = 1.0f / 8192.0f;         // E / (|q| max |k|), see 
 // blocks, in shared memory).  One pass then turns the scores into a bit per
 // block (sure, candidate; 8 chunks a word); what follows loops over those words:
 // code that is unrolled over the row more often does not fit the instruction
-// cache.  A few candidates are ranked directly, a lane each; more than kSelKeys
+// cache (640 against 305 us for 12 x 1536 rows of 1536 blocks; 130 us as it is,
+// half of it issue slots, the rest waits for the few 64-bit means).  A few candidates are ranked directly, a lane each; more than kSelKeys
 // (rows of equal scores) by bisection over their keys, which then lie in memory
 // that is the row's own: the rough scores, no longer needed, and the output
 // list, not yet written.
@@ -373,59 +357,94 @@ blockmean_select_kernel(const double* __restrict__ mean, const double* __restric
   auto mixed = [&](int i) -> bool { return 128 * i + 128 > nB || (128 * i + 128 > f0 && 128 * i < f1); };
 
   if (rough) {
-    // rough scores; out of the choice: -infinity
+    // rough scores; out of the choice: -infinity.  Their extremes, and mean and
+    // deviation from one of them (which keeps the digits of close scores)
     float4 v[C4 ? C4 : 1];
     float lo = INFINITY, hi = -INFINITY;
+    const float x0 = __ldcg(row + (f0 > 0 ? 0 : f1));
+    const uint64_t nx0 = f2pack(-x0, -x0);
+    uint64_t s1 = f2pack(0.f, 0.f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < chunks; ++i) {
       const int j = 128 * i + 4 * lane;
-      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      float4 x = make_float4(x0, x0, x0, x0);
       if (j < nB) x = __ldcg(reinterpret_cast<const float4*>(row + j));
-      float mn;
+      if (mixed(i)) {                                 // blocks that do not count stand at x0 for a moment
+        const bool a = j >= nB || own(j), b = j + 1 >= nB || own(j + 1), c = j + 2 >= nB || own(j + 2),
+                   e = j + 3 >= nB || own(j + 3);
+        x = make_float4(a ? x0 : x.x, b ? x0 : x.y, c ? x0 : x.z, e ? x0 : x.w);
+      }
+      lo = fminf(lo, fminf(fminf(x.x, x.y), fminf(x.z, x.w)));
+      hi = fmaxf(hi, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+      const uint64_t d0 = fadd2(f2pack(x.x, x.y), nx0), d1 = fadd2(f2pack(x.z, x.w), nx0);
+      s1 = fadd2(s1, fadd2(d0, d1));
+      s2 = ffma2(d1, d1, ffma2(d0, d0, s2));
       if (mixed(i)) {
         const bool a = j >= nB || own(j), b = j + 1 >= nB || own(j + 1), c = j + 2 >= nB || own(j + 2),
                    e = j + 3 >= nB || own(j + 3);
-        mn = fminf(fminf(a ? INFINITY : x.x, b ? INFINITY : x.y), fminf(c ? INFINITY : x.z, e ? INFINITY : x.w));
         x = make_float4(a ? -INFINITY : x.x, b ? -INFINITY : x.y, c ? -INFINITY : x.z, e ? -INFINITY : x.w);
-      } else {
-        mn = fminf(fminf(x.x, x.y), fminf(x.z, x.w));
       }
-      lo = fminf(lo, mn);
-      hi = fmaxf(hi, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
       if (C4) v[C4 ? i : 0] = x;
       else if (j < nB) srow[j / 4] = x;
     }
     lo = -warp_max_f(-lo);
     hi = warp_max_f(hi);
+    const float mean_d = warp_sum_f(f2sum(s1)) / rest;
+    const float sd = sqrtf(fmaxf(warp_sum_f(f2sum(s2)) / rest - mean_d * mean_d, 0.f));
     __syncwarp();
     auto score = [&](int i) -> float4 {
       if (C4) return v[C4 ? i : 0];
       if (128 * i + 4 * lane < nB) return srow[32 * i + lane];
       return make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     };
-    const float e = static_cast<float>(scale) * kRoughError;
-    // count(lo) >= take > count(hi), count(t) = blocks with a score >= t: the
-    // take-th largest lies in [lo, hi)
-    int nlo = rest, nhi = 0;
-    hi = hi + fmaxf(e, 1e-6f * fabsf(hi));
-    for (int step = 0; nlo - nhi > 1 && hi - lo > e; ++step) {
-      // by the counts' proportion, every third time in the middle
-      const float part = step % 3 == 2 ? 0.5f : (nlo - take + 0.5f) / (nlo - nhi);
-      const float mid = lo + fminf(fmaxf(part, 0.02f), 0.98f) * (hi - lo);
-      if (!(mid > lo && mid < hi)) break;
-      int n = 0;
+    // blocks with a score >= t: all positions less those whose difference has
+    // its sign bit set (one packed subtraction and an add for each)
+    auto count = [&](float t) -> int {
+      const uint64_t nt = f2pack(-t, -t);
+      uint32_t below = 0;
 #pragma unroll
       for (int i = 0; i < chunks; ++i) {
         const float4 x = score(i);
-        n += (x.x >= mid ? 1 : 0) + (x.y >= mid ? 1 : 0) + (x.z >= mid ? 1 : 0) + (x.w >= mid ? 1 : 0);
+        float a, b, c, e;
+        f2unpack(fadd2(f2pack(x.x, x.y), nt), a, b);
+        f2unpack(fadd2(f2pack(x.z, x.w), nt), c, e);
+        below += __float_as_uint(a) >> 31;
+        below += __float_as_uint(b) >> 31;
+        below += __float_as_uint(c) >> 31;
+        below += __float_as_uint(e) >> 31;
       }
-      n = __reduce_add_sync(kAll, n);
+      return 128 * chunks - static_cast<int>(__reduce_add_sync(kAll, below));
+    };
+    const float e = static_cast<float>(scale) * kRoughError;
+    // count(lo) >= take > count(hi): the take-th largest lies in [lo, hi).  The
+    // first steps go where a normal distribution of the row's mean and deviation
+    // would put it, each then by the density there and a little beyond; later
+    // ones by the counts' proportion, every third in the middle.  (6 steps on
+    // average over normal rows of 1536, where halving takes 12.)
+    int nlo = rest, nhi = 0;
+    hi = hi + fmaxf(e, 1e-6f * fabsf(hi));
+    float z = normcdfinvf(1.f - static_cast<float>(take) / rest);
+    for (int step = 0; nlo - nhi > 1 && hi - lo > e; ++step) {
+      const float mean_x = x0 + mean_d;
+      float mid = fmaf(z, sd, mean_x);
+      if (step > 5 || !(mid > lo && mid < hi)) {
+        const float part = step % 3 == 2 ? 0.5f : (nlo - take + 0.5f) / (nlo - nhi);
+        mid = lo + fminf(fmaxf(part, 0.02f), 0.98f) * (hi - lo);
+      }
+      if (!(mid > lo && mid < hi)) break;
+      const int n = count(mid);
       if (n >= take) {
         lo = mid;
         nlo = n;
       } else {
         hi = mid;
         nhi = n;
+      }
+      if (step <= 5) {
+        const float miss = static_cast<float>(n - take);            // > 0: the threshold is higher
+        const float zz = (mid - mean_x) / sd;
+        const float density = rest * 0.3989423f * __expf(-0.5f * zz * zz);
+        z = zz + (miss + (miss >= 0.f ? 1.f : -1.f) * fmaf(0.05f, fabsf(miss), 1.f)) / density;
       }
     }
     // the take-th largest rough score is within [lo, hi), the exact one within

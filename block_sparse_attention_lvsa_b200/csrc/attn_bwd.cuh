@@ -53,11 +53,12 @@ struct BwdParams {
   const uint8_t* flags;
   long long lhs;
   int lrs, chs;
-  // dkv: query-tile lists of the key tiles, entry = tile | partial << 30
-  const int32_t* tlist;
-  const int32_t* tcount;
-  long long tlhs;                   // head stride (0: shared by all heads)
-  int tchs;
+  // dkv: bit sets of the lists [heads or 1][nW][nB] (part: null without flags)
+  // and room for the query-tile lists of the key tiles [H][nB][nB]
+  const uint32_t* bits;
+  const uint32_t* part;
+  long long bhs;                    // head stride of the bit sets (0: shared by all heads)
+  int32_t* tlist;
   // element mask (LVSA)
   const uint32_t* fbits;
   int TW, P;
@@ -116,88 +117,63 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return v;
 }
 
-// Bit sets of the rows' lists: bits[h][w][qb] bit b = key tile 32 w + b is
-// listed by query tile qb, and the same of the partial ones.  One warp per
-// row; 8192 tiles at a time in shared memory.  Entries out of range are
-// skipped and, like repeated ones, reported.
-__global__ void __launch_bounds__(128) attn_bwd_bits_kernel(const int32_t* __restrict__ list,
-                                                            const int32_t* __restrict__ count,
-                                                            const uint8_t* __restrict__ flags, long long lhs, int lrs,
-                                                            int chs, int nB, uint32_t* __restrict__ bits,
-                                                            uint32_t* __restrict__ part) {
-  constexpr int kWords = 256;
-  __shared__ uint32_t s_on[4][kWords], s_part[4][kWords];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qb = blockIdx.x * 4 + warp, h = blockIdx.y;
-  if (qb >= nB) return;
-  const int nW = (nB + 31) / 32;
-  int n = count[static_cast<size_t>(h) * chs + qb];
-  bool bad = n < 0 || n > lrs;
-  n = min(max(n, 0), lrs);
-  const size_t off = static_cast<size_t>(h) * lhs + static_cast<size_t>(qb) * lrs;
-  for (int w0 = 0; w0 < nW; w0 += kWords) {
-    const int words = min(kWords, nW - w0);
-    for (int w = lane; w < words; w += 32) s_on[warp][w] = s_part[warp][w] = 0u;
-    __syncwarp();
-    for (int j = lane; j < n; j += 32) {
-      const int kt = list[off + j];
-      if (kt < 0 || kt >= nB) {
-        bad = true;
-        continue;
-      }
-      const int w = (kt >> 5) - w0;
-      if (w < 0 || w >= words) continue;
-      const uint32_t b = 1u << (kt & 31);
-      if (atomicOr(&s_on[warp][w], b) & b) bad = true;
-      if (flags != nullptr && flags[off + j]) atomicOr(&s_part[warp][w], b);
-    }
-    __syncwarp();
-    for (int w = lane; w < words; w += 32) {
-      const size_t at = (static_cast<size_t>(h) * nW + w0 + w) * nB + qb;
-      bits[at] = s_on[warp][w];
-      if (part != nullptr) part[at] = s_part[warp][w];
-    }
-    __syncwarp();
-  }
-  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(BSA_ERR_INDEX_RANGE);
-}
-
 // Two independent preparations in one launch, 256 threads a block.
-// Blocks below `list_blocks`: the query-tile lists of the key tiles, ascending,
-// one warp per key tile of a head, 32 query tiles a step.
+// Blocks below `bit_blocks`: bit sets of the rows' lists, bits[h][w][qb] bit b =
+// key tile 32 w + b is listed by query tile qb, and the same of the partial
+// ones.  One warp per row; 8192 tiles at a time in shared memory.  Entries out
+// of range are skipped and, like repeated ones, reported.
 // The others: nl = -lse * log2(e) and nd = -<do, o> per (head, token),
 // [H][nB * 128]; tokens past N and rows without a key get nl = -inf (p = 0);
 // d/8 lanes a row.
 template <int D>
 __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(
-    int nB, int list_heads, unsigned list_blocks, const uint32_t* __restrict__ bits, const uint32_t* __restrict__ part,
-    int32_t* __restrict__ tlist, int32_t* __restrict__ tcount, const __nv_bfloat16* __restrict__ o, long long o_ts,
-    long long o_hs, const __nv_bfloat16* __restrict__ go, const float* __restrict__ lse, int N, int H,
-    float* __restrict__ nl, float* __restrict__ nd) {
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x < list_blocks) {
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);   // h * nB + key tile
+    const int32_t* __restrict__ list, const int32_t* __restrict__ count, const uint8_t* __restrict__ flags,
+    long long lhs, int lrs, int chs, int nB, int list_heads, unsigned bit_blocks, uint32_t* __restrict__ bits,
+    uint32_t* __restrict__ part, const __nv_bfloat16* __restrict__ o, long long o_ts, long long o_hs,
+    const __nv_bfloat16* __restrict__ go, const float* __restrict__ lse, int N, int H, float* __restrict__ nl,
+    float* __restrict__ nd) {
+  constexpr int kWords = 256;
+  __shared__ uint32_t s_on[8][kWords], s_part[8][kWords];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x < bit_blocks) {
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + warp;              // h * nB + query tile
     if (row >= static_cast<long long>(list_heads) * nB) return;
-    const int h = static_cast<int>(row / nB), kt = static_cast<int>(row - static_cast<long long>(h) * nB);
-    const size_t at = (static_cast<size_t>(h) * ((nB + 31) / 32) + (kt >> 5)) * nB;
-    int32_t* out = tlist + static_cast<size_t>(row) * nB;
-    int n = 0;
-    for (int q0 = 0; q0 < nB; q0 += 32) {
-      const int qb = q0 + lane;
-      const bool on = qb < nB && ((bits[at + qb] >> (kt & 31)) & 1u);
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
-      if (on) {
-        const bool partial = part != nullptr && ((part[at + qb] >> (kt & 31)) & 1u);
-        out[n + __popc(m & ((1u << lane) - 1u))] = qb | (partial ? kPartialBit : 0);
+    const int h = static_cast<int>(row / nB), qb = static_cast<int>(row - static_cast<long long>(h) * nB);
+    const int nW = (nB + 31) / 32;
+    int n = count[static_cast<size_t>(h) * chs + qb];
+    bool bad = n < 0 || n > lrs;
+    n = min(max(n, 0), lrs);
+    const size_t off = static_cast<size_t>(h) * lhs + static_cast<size_t>(qb) * lrs;
+    for (int w0 = 0; w0 < nW; w0 += kWords) {
+      const int words = min(kWords, nW - w0);
+      for (int w = lane; w < words; w += 32) s_on[warp][w] = s_part[warp][w] = 0u;
+      __syncwarp();
+      for (int j = lane; j < n; j += 32) {
+        const int kt = list[off + j];
+        if (kt < 0 || kt >= nB) {
+          bad = true;
+          continue;
+        }
+        const int w = (kt >> 5) - w0;
+        if (w < 0 || w >= words) continue;
+        const uint32_t b = 1u << (kt & 31);
+        if (atomicOr(&s_on[warp][w], b) & b) bad = true;
+        if (flags != nullptr && flags[off + j]) atomicOr(&s_part[warp][w], b);
       }
-      n += __popc(m);
+      __syncwarp();
+      for (int w = lane; w < words; w += 32) {
+        const size_t at = (static_cast<size_t>(h) * nW + w0 + w) * nB + qb;
+        bits[at] = s_on[warp][w];
+        if (part != nullptr) part[at] = s_part[warp][w];
+      }
+      __syncwarp();
     }
-    if (lane == 0) tcount[row] = n;
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(BSA_ERR_INDEX_RANGE);
     return;
   }
   constexpr int G = D / 8;
   const int NP = nB * 128;
-  const long long row = (static_cast<long long>(blockIdx.x - list_blocks) * 256 + threadIdx.x) / G;   // n * H + h
+  const long long row = (static_cast<long long>(blockIdx.x - bit_blocks) * 256 + threadIdx.x) / G;   // n * H + h
   const int l = threadIdx.x % G;
   const int n = static_cast<int>(row / H);
   const int h = static_cast<int>(row - static_cast<long long>(n) * H);
@@ -220,6 +196,33 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(
     nl[at] = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
     nd[at] = -sum;
   }
+}
+
+// The query tiles that list key tile kt, ascending, entry = tile | partial <<
+// 30, by one warp from the bit sets (`bits`, `part`: the head's).  Returns
+// their number.
+__device__ __forceinline__ int listed_by(const uint32_t* bits, const uint32_t* part, int nB, int kt, int32_t* out,
+                                         int lane) {
+  const size_t at = static_cast<size_t>(kt >> 5) * nB;
+  int n = 0;
+#pragma unroll 4
+  for (int q0 = 0; q0 < nB; q0 += 32) {
+    const int qb = q0 + lane;
+    const uint32_t a = qb < nB ? __ldg(bits + at + qb) : 0u;
+    const uint32_t b = (part != nullptr && qb < nB) ? __ldg(part + at + qb) : 0u;
+    const bool on = (a >> (kt & 31)) & 1u;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
+    if (on) out[n + __popc(m & ((1u << lane) - 1u))] = qb | (((b >> (kt & 31)) & 1u) ? kPartialBit : 0);
+    n += __popc(m);
+  }
+  return n;
+}
+// a list entry written by this block (not through the read-only path), loaded
+// where the call stands
+__device__ __forceinline__ int32_t ld_entry(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t bits32(int a, int b) {          // bits a .. b - 1, 0 <= a < b <= 32
@@ -321,8 +324,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = p.wait_limit_ns;
-  const int n = p.tcount[static_cast<size_t>(h) * p.tchs + kt];
-  const int32_t* lst = p.tlist + static_cast<size_t>(h) * p.tlhs + static_cast<size_t>(kt) * p.nB;
+  int32_t* lst = p.tlist + (static_cast<size_t>(h) * p.nB + kt) * p.nB;
   const int NP = p.nB * 128;
 
   if (threadIdx.x == 0) {
@@ -341,10 +343,16 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
     tmem_alloc(base + L::kHolder, 512);
     tmem_relinquish();
   }
+  if (warp == 2) {
+    const size_t off = static_cast<size_t>(h) * p.bhs;
+    const int c = listed_by(p.bits + off, p.part != nullptr ? p.part + off : nullptr, p.nB, kt, lst, lane);
+    if (lane == 0) holder[1] = static_cast<uint32_t>(c);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *holder;
+  const uint32_t tbase = holder[0];
+  const int n = static_cast<int>(holder[1]);
   // d = 64 leaves room for two dP, so that dP(i+1) need not wait for dK(i)
   constexpr int kDP = D == 64 ? 2 : 1;
   constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 128 + 128 * kDP, kTDK = kTDV + D;
@@ -361,7 +369,7 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
       int nq = 0, no = 0;                               // copies started
       bool ok = true;
       for (int i = 0; i < n; ++i) {
-        const int qt = lst[i] & ~kPartialBit;
+        const int qt = ld_entry(lst + i) & ~kPartialBit;
         if (i >= 3) ok = mbar_wait(bar(W_QEMPTY + i % 3), (i / 3 - 1) & 1, limit);
         if (!ok) break;
         mbar_arrive_expect_tx(bar(W_QFULL + i % 3), L::kTile);
@@ -458,10 +466,10 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
     const int fk = p.fbits != nullptr ? min(kt * 128 + r, p.N - 1) / p.P : 0;
     const uint64_t sl2p = f2pack(p.sl2, p.sl2);
     bool ok = true;
-    int e_next = n > 0 ? ld_pinned_s32(lst) : 0;
+    int e_next = n > 0 ? ld_entry(lst) : 0;
     for (int i = 0; ok && i < n; ++i) {
       const int e = e_next;
-      if (i + 1 < n) e_next = ld_pinned_s32(lst + i + 1);
+      if (i + 1 < n) e_next = ld_entry(lst + i + 1);
       const bool part = (e & kPartialBit) != 0 && p.fbits != nullptr;
       uint32_t mw = 0xFFFFFFFFu;
       if (part) mw = query_mask(p, fk, (e & ~kPartialBit) * 128 + kBwdCols * g);

@@ -175,10 +175,10 @@ size_t index_ws_bytes(const bsa_index* index, int N, int H) {
 }
 
 // Workspace of the attention's gradient: the index's own part, the padded
-// per-row values, the bit sets of the lists and the lists the other way round
-// (shared by all heads for LVSA frame indexes).
+// per-row values, the bit sets of the lists (shared by all heads for LVSA frame
+// indexes) and room for the lists the other way round.
 struct BwdWs {
-  size_t nl, nd, bits, part, tcnt, tlist, total;
+  size_t nl, nd, bits, part, tlist, total;
   int lists;                        // heads with lists of their own (1: shared)
 };
 BwdWs bwd_ws_layout(const bsa_index* index, int N, int H) {
@@ -196,9 +196,8 @@ BwdWs bwd_ws_layout(const bsa_index* index, int N, int H) {
   w.nd = w.nl + static_cast<size_t>(H) * nB * 128 * 4;
   w.bits = w.nd + static_cast<size_t>(H) * nB * 128 * 4;
   w.part = round_up(w.bits + lists * nW * nB * 4, 256);
-  w.tcnt = index->kind == BSA_INDEX_BLOCKS ? w.part : round_up(w.part + lists * nW * nB * 4, 256);
-  w.tlist = round_up(w.tcnt + lists * nB * 4, 256);
-  w.total = round_up(w.tlist + lists * nB * nB * 4, 256);
+  w.tlist = index->kind == BSA_INDEX_BLOCKS ? w.part : round_up(w.part + lists * nW * nB * 4, 256);
+  w.total = round_up(w.tlist + static_cast<size_t>(H) * nB * nB * 4, 256);
   return w;
 }
 
@@ -1024,27 +1023,20 @@ extern "C" int blocksparse_attn_bwd(const void* go, const void* q, const void* k
   float* nd = reinterpret_cast<float*>(ws + w.nd);
   uint32_t* bits = reinterpret_cast<uint32_t*>(ws + w.bits);
   uint32_t* part = a.flags ? reinterpret_cast<uint32_t*>(ws + w.part) : nullptr;
-  int32_t* tcnt = reinterpret_cast<int32_t*>(ws + w.tcnt);
-  int32_t* tlist = reinterpret_cast<int32_t*>(ws + w.tlist);
   p.nl = nl;
   p.nd = nd;
-  p.tlist = tlist;
-  p.tcount = tcnt;
-  p.tlhs = w.lists == 1 ? 0 : static_cast<long long>(nB) * nB;
-  p.tchs = w.lists == 1 ? 0 : nB;
-  attn_bwd_bits_kernel<<<dim3((nB + 3) / 4, w.lists), 128, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB,
-                                                                   bits, part);
-  const unsigned list_blocks = static_cast<unsigned>((static_cast<long long>(w.lists) * nB + 7) / 8);
+  p.bits = bits;
+  p.part = part;
+  p.bhs = w.lists == 1 ? 0 : static_cast<long long>((nB + 31) / 32) * nB;
+  p.tlist = reinterpret_cast<int32_t*>(ws + w.tlist);
+  const unsigned bit_blocks = static_cast<unsigned>((static_cast<long long>(w.lists) * nB + 7) / 8);
   const long long lanes = static_cast<long long>(nB) * 128 * H * (d / 8);
-  const unsigned blocks = list_blocks + static_cast<unsigned>((lanes + 255) / 256);
+  const unsigned blocks = bit_blocks + static_cast<unsigned>((lanes + 255) / 256);
   const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o->data);
   const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(go);
-  if (d == 128)
-    attn_bwd_prep_kernel<128><<<blocks, 256, 0, st>>>(nB, w.lists, list_blocks, bits, part, tlist, tcnt, ob,
-                                                      o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
-  else
-    attn_bwd_prep_kernel<64><<<blocks, 256, 0, st>>>(nB, w.lists, list_blocks, bits, part, tlist, tcnt, ob,
-                                                     o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
+  auto* prep = d == 128 ? attn_bwd_prep_kernel<128> : attn_bwd_prep_kernel<64>;
+  prep<<<blocks, 256, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB, w.lists, bit_blocks, bits, part, ob,
+                               o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
   return d == 128 ? launch_bwd<128>(go, q, k, v, N, H, p, dq, dk, dv, st)
                   : launch_bwd<64>(go, q, k, v, N, H, p, dq, dk, dv, st);

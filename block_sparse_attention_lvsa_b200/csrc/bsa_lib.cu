@@ -955,7 +955,10 @@ int launch_bwd(const void* go, const void* q, const void* k, const void* v, int 
       !make_qkv_map(&mdq, dq, N, H, D, 128) || !make_qkv_map(&mdk, dk, N, H, D, 128) ||
       !make_qkv_map(&mdv, dv, N, H, D, 128))
     return BSA_ERR_CUDA;
-  attn_bwd_kernel<D><<<dim3(2 * p.nB, H), kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, mdk, mdv, p);
+  // all key tiles first where the blocks fill the SMs fewer than eight times
+  const bool apart = 2LL * p.nB * H < 8 * 148;
+  const dim3 grid(apart ? p.nB : 2 * p.nB, H, apart ? 2 : 1);
+  attn_bwd_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, mdk, mdv, p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

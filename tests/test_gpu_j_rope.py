@@ -116,6 +116,8 @@ CASES = [
     ((4, 9, 3), 5, 9, 64, "fp32", "adjacent", "packed", True),
     ((4, 9, 3), 0, 17, 64, "fp16", "adjacent", "heads first", False),
     ((1, 17, 1), 0, 8, 128, "fp32", "split", "whole", True),
+    ((1, 1, 1), 0, 100, 128, "bf16", "adjacent", "whole", False),     # one token: its heads in several blocks
+    ((2, 1, 1), 1, 33, 64, "fp32", "adjacent", "heads first", True),
 ]
 
 

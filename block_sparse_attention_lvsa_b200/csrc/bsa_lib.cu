@@ -805,7 +805,7 @@ constexpr size_t kMeanPassBytes = size_t(64) << 20;
 MeanWs mean_ws_layout(int N, int H, int d) {
   const size_t nB = static_cast<size_t>(n_tiles(N)), elems = static_cast<size_t>(2) * H * nB * d;
   MeanWs w;
-  w.ldS = static_cast<int>(round_up(nB, 4));
+  w.ldS = static_cast<int>(round_up(nB, 8));          // rows of whole 32-byte sectors
   w.per_head = nB * w.ldS * 4;
   w.heads = static_cast<int>(std::max<size_t>(1, std::min<size_t>(H, kMeanPassBytes / w.per_head)));
   w.mean = 0;
@@ -817,16 +817,16 @@ MeanWs mean_ws_layout(int N, int H, int d) {
   return w;
 }
 
-bool make_map_3d(CUtensorMap* m, CUtensorMapDataType type, int es, const void* ptr, cuuint64_t x, cuuint64_t y,
-                 cuuint64_t z, cuuint64_t pitch, cuuint32_t bx) {
+// (d, nB, heads) of a bf16 [heads][nB][d] array, boxes of 64 x 128 x 1
+bool make_means_map(CUtensorMap* m, const void* ptr, int d, int nB, int heads) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {x, y, z};
-  cuuint64_t strides[2] = {pitch * es, y * pitch * es};
-  cuuint32_t box[3] = {bx, 128, 1};
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(nB), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(nB) * d * 2};
+  cuuint32_t box[3] = {64, 128, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -883,16 +883,14 @@ int launch_mean(const MeanWs& w, uint8_t* ws, int H, int nB, int keep, int local
   int rc = allow_smem(blockmean_score_kernel<D>, static_cast<int>(ScoreSmem<D>::kAlloc), done);
   if (rc != BSA_OK) return rc;
   CUtensorMap mh, ml;
-  if (!make_map_3d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ws + w.hi, D, nB, 2ull * H, D, 64) ||
-      !make_map_3d(&ml, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ws + w.lo, D, nB, 2ull * H, D, 64))
+  if (!make_means_map(&mh, ws + w.hi, D, nB, 2 * H) || !make_means_map(&ml, ws + w.lo, D, nB, 2 * H))
     return BSA_ERR_CUDA;
   const unsigned tiles = static_cast<unsigned>((nB + 127) / 128);
   for (int h0 = 0; h0 < H; h0 += w.heads) {
     const int hn = std::min(w.heads, H - h0);
-    CUtensorMap ms;
-    if (!make_map_3d(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + w.scores, nB, nB, hn, w.ldS, 32)) return BSA_ERR_CUDA;
-    blockmean_score_kernel<D><<<dim3(tiles, tiles, hn), kScoreThreads, ScoreSmem<D>::kAlloc, st>>>(mh, ml, ms, H, h0, nB,
-                                                                                              kWaitLimitNs);
+    const dim3 grid((tiles + kScoreTiles - 1) / kScoreTiles, tiles, hn);
+    blockmean_score_kernel<D><<<grid, kScoreThreads, ScoreSmem<D>::kAlloc, st>>>(
+        mh, ml, reinterpret_cast<float*>(ws + w.scores), w.ldS, H, h0, nB, kWaitLimitNs);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (nB <= 256) rc = launch_mean_select<D, 2>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);
     else if (nB <= 512) rc = launch_mean_select<D, 4>(w, ws, H, h0, hn, nB, keep, local, idx, cnt, st);

@@ -258,6 +258,39 @@ def test_many_calls_in_a_row(bsa):
         assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+def test_two_streams_at_once(bsa):
+    """The whole chain on two streams at the same time, scratch from each stream's own pool."""
+    N, H, d = 3000, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(95)
+    x = [torch.randn((N, 3, H, d), generator=g, device="cuda").bfloat16() for _ in range(2)]
+    go = torch.randn((N, H, d), generator=g, device="cuda").bfloat16()
+    w = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    rope = bsa.rope_axes([bsa.rope_build_table(n, p, device="cuda") for n, p in zip((30, 10, 10), (22, 21, 21))],
+                         grid=(30, 10, 10))
+
+    def chain(x, stream):
+        with torch.cuda.stream(stream):
+            v = x[:, 2].contiguous()
+            q, k = bsa.qk_norm_rope_fwd(x[:, 0], x[:, 1], w, w, rope)
+            idx, cnt = bsa.blockmean_select(q, k, 6, 1)
+            o, lse, grads = both(bsa, go, q, k, v, bsa.block_index(idx, cnt))
+            return (q, k, idx, cnt, o, *grads, *bsa.qk_norm_rope_bwd(grads[0], grads[1], x[:, 0], x[:, 1], w, w, rope))
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    ref = []
+    for i in range(2):
+        ref.append(chain(x[i], streams[i]))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        got = [chain(x[i], streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    assert bsa.get_device_status() == bsa.BSA_OK
+    for a, b in zip(ref, got):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
 def test_against_differences_of_the_oracle(bsa):
     """Directional central differences of the float64 forward; the gradient's own
     tolerance is the bound above, summed along the direction."""

@@ -24,7 +24,8 @@
 //     kept, one below t - 2E is not, and only those between (a few of 1536)
 //     get 64-bit scores.  Rows whose norms leave the range where these bounds
 //     hold (32-bit products near the ends of the exponent, values that are not
-//     finite) get 64-bit scores throughout.
+//     finite), and calls with so few blocks that there are no rough scores, get
+//     64-bit scores throughout.
 #pragma once
 #include "rope.cuh"   // packed pairs of float
 
@@ -380,7 +381,7 @@ blockmean_select_kernel(const double* __restrict__ mean, const double* __restric
   const int take = min(nB, max(keep, forced)) - forced;        // blocks chosen by score
   const double qn = norm[static_cast<size_t>(h) * nB + qb], scale = qn * kmax;
   const bool choose = take > 0 && take < rest;
-  const bool rough = choose && kfin && isfinite(qn) && qn >= 1e-25 && kmax >= 1e-25 && scale >= 1e-25 && scale <= 1e30;
+  const bool rough = choose && scores != nullptr && kfin && isfinite(qn) && qn >= 1e-25 && kmax >= 1e-25 && scale >= 1e-25 && scale <= 1e30;
   auto own = [&](int j) -> bool { return j >= f0 && j < f1; };
   // chunk i holds blocks that take no part in the choice
   auto mixed = [&](int i) -> bool { return 128 * i + 128 > nB || (128 * i + 128 > f0 && 128 * i < f1); };

@@ -36,7 +36,14 @@
  *  - No C++ exception crosses this interface.
  *  - Supported: batch 1, bfloat16 inputs, d in {64, 128}, N >= 1,
  *    N * H * d < 2^31, 16-byte aligned q/k/v/o.  Anything else returns
- *    BSA_ERR_UNSUPPORTED or BSA_ERR_ARG.
+ *    BSA_ERR_UNSUPPORTED or BSA_ERR_ARG.  The rotation calls (rope_*,
+ *    qk_norm_rope_*) also take float16 and float32, strides, and sizes past
+ *    2^31 elements (see bsa_heads).
+ *
+ * Around the attention: rope_build_table, rope_apply, qk_norm_rope_fwd / _bwd
+ * (rotary positions over time, height and width, with the per-head norm of q
+ * and k), blockmean_select (key blocks by block means), blocksparse_attn_bwd
+ * (the attention's gradient).
  */
 #ifndef BSA_H_
 #define BSA_H_
@@ -496,6 +503,8 @@ enum {
  * BSA_OP_DENSE_BLOCKMASS the answer is the share of as many heads as fit in
  * 4 GiB (at least one, at most H), share = ceil(N/128) * N * 4 bytes; any
  * workspace of at least one share is accepted by attn_dense_blockmass.
+ * BSA_OP_BLOCKSPARSE_BWD: all that blocksparse_attn_bwd needs, dominated by
+ * H * ceil(N/128)^2 * 4 bytes of lists.
  * Returns (size_t)-1 for invalid arguments.
  */
 size_t bsa_workspace_bytes(int op, int N, int H, int d, const bsa_index* index);

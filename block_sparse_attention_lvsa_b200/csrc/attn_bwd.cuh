@@ -2,7 +2,7 @@
 // tensor cores (tcgen05 + TMEM + TMA).
 //
 // With s = scale <q, k>, p = exp(s - lse) the forward's probabilities and
-// D_q = <do_q, o_q> = sum_k p <do_q, v_k>:
+// D_q = <do_q, o_q> = sum_k p <do_q, v_k> (the second form for rows of few keys):
 //   dv_k = sum_q p do_q
 //   ds   = p (<do_q, v_k> - D_q)
 //   dq_q = scale sum_k ds k_k,     dk_k = scale sum_q ds q_q
@@ -117,26 +117,127 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return v;
 }
 
-// Two independent preparations in one launch, 256 threads a block.
+__device__ __forceinline__ uint32_t bits32(int a, int b) {          // bits a .. b - 1, 0 <= a < b <= 32
+  return (b - a == 32 ? 0xFFFFFFFFu : (1u << (b - a)) - 1u) << a;
+}
+__device__ __forceinline__ bool frame_bit(const BwdParams& p, int fq, int fk) {
+  return (__ldg(p.fbits + static_cast<size_t>(fq) * p.TW + (fk >> 5)) >> (fk & 31)) & 1u;
+}
+// Element mask of 32 query columns for key frame fk: bit c set iff query q0+c
+// < N may attend it.
+__device__ __forceinline__ uint32_t query_mask(const BwdParams& p, int fk, int q0) {
+  uint32_t m = 0u;
+  const int qend = min(q0 + kBwdCols, p.N);
+  for (int f = q0 / p.P; f * p.P < qend; ++f)
+    if (frame_bit(p, f, fk)) m |= bits32(max(f * p.P, q0) - q0, min((f + 1) * p.P, qend) - q0);
+  return m;
+}
+// Element mask of 32 key columns for query frame fq (no frames: every key < N).
+__device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0) {
+  uint32_t m = 0u;
+  const int kend = min(k0 + kBwdCols, p.N);
+  if (p.fbits == nullptr) return k0 < kend ? bits32(0, kend - k0) : 0u;
+  for (int f = k0 / p.P; f * p.P < kend; ++f)
+    if (frame_bit(p, fq, f)) m |= bits32(max(f * p.P, k0) - k0, min((f + 1) * p.P, kend) - k0);
+  return m;
+}
+
+// Rows of few keys.  <do, o> with o rounded to bf16 is off by up to 2^-8 of
+// sum |do| |o|, next to differences <do, v_k> - D that, with two or three keys,
+// can all be small: dq and dk of 2 tokens were off by up to 6e-2 of their norm.
+// Up to kFewKeys keys D is therefore formed anew in 32 bits,
+//   D = sum p <do, v_k> / sum p,
+// from which the sum of ds over the row vanishes as it should.  The rounding of
+// o averages out over the keys: with 32 or more it adds less to the error of
+// the gradients (3.1e-3 to 3.6e-3 of their norm with 16 keys, 2.6e-3 to 3.0e-3
+// with 64) than the rounding of p and ds (2.4e-3).  A row of one key has p = 1
+// and ds = 0 whatever dP is; where such rows can fill the input (`ones`: frames
+// of one token, a last block of one key) they get the mark kOneKey in place of
+// -D, a NaN that no arithmetic gives, at which ds is set to 0.  Elsewhere the
+// check would cost 5% (947 against 889 us, 161 blocks, 12 heads, d = 128).
+constexpr int kFewKeys = 32;
+constexpr uint32_t kOneKey = 0x7FC00001u;
+// What it costs the whole gradient: 10.6 -> 16.6 us where every row has 32 keys
+// (32 tokens, 6 heads, d = 128; 20.8 with 8 keys in flight, and blocks of 256
+// threads leave SMs idle), 36.7 -> 38.4 us where a short last block only may make
+// such rows (4,104 tokens); nothing where the sizes exclude them.
+constexpr int prep_threads(bool few) { return few ? 64 : 256; }
+
+// The keys of query n of head h by its list, if there are 1 to kFewKeys, into
+// `keys`: their number, or 0.  Called by a group of G lanes (mask `gm`, lane l
+// of it): lanes 0..3 take 32 columns of a tile each.
+template <int G>
+__device__ __forceinline__ int few_keys(const BwdParams& p, int n, int h, unsigned gm, int l, int32_t* keys) {
+  const int qt = n >> 7;
+  const int m = min(max(p.count[static_cast<size_t>(h) * p.chs + qt], 0), p.lrs);
+  const size_t off = static_cast<size_t>(h) * p.lhs + static_cast<size_t>(qt) * p.lrs;
+  const int fq = p.fbits != nullptr ? n / p.P : 0;
+  int total = 0;
+  for (int j = 0; j < m; ++j) {
+    const int kt = p.list[off + j];
+    if (kt < 0 || kt >= p.nB) continue;
+    const int k0 = kt * 128 + 32 * l;
+    uint32_t w = 0u;
+    if (l < 4 && k0 < p.N) {
+      // a tile that is not partial holds 128 keys
+      const bool part = p.flags != nullptr ? p.flags[off + j] != 0 : kt * 128 + 128 > p.N;
+      w = part ? key_mask(p, fq, k0) : 0xFFFFFFFFu;
+    }
+    const int c = __popc(w);
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ci = __shfl_sync(gm, c, i, G);
+      before += i < l ? ci : 0;
+      sum += ci;
+    }
+    if (total + sum > kFewKeys) return 0;
+    for (int at = total + before; w != 0u; w &= w - 1u) keys[at++] = k0 + __ffs(w) - 1;
+    total += sum;
+  }
+  __syncwarp(gm);
+  return total;
+}
+
+// a 16-byte load that stays where the call stands (several in flight)
+__device__ __forceinline__ uint4 ld_pinned_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// <x, y> over 8 channels in bf16
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+    sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
+  }
+  return sum;
+}
+
+// Two independent preparations in one launch, 256 threads a block (FEW: 64).
 // Blocks below `bit_blocks`: bit sets of the rows' lists, bits[h][w][qb] bit b =
 // key tile 32 w + b is listed by query tile qb, and the same of the partial
 // ones.  One warp per row; 8192 tiles at a time in shared memory.  Entries out
 // of range are skipped and, like repeated ones, reported.
-// The others: nl = -lse * log2(e) and nd = -<do, o> per (head, token),
+// The others: nl = -lse * log2(e) and nd = -D per (head, token),
 // [H][nB * 128]; tokens past N and rows without a key get nl = -inf (p = 0);
-// d/8 lanes a row.
-template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_prep_kernel(
+// d/8 lanes a row.  FEW: rows of at most kFewKeys keys may occur.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(prep_threads(FEW)) attn_bwd_prep_kernel(
     const int32_t* __restrict__ list, const int32_t* __restrict__ count, const uint8_t* __restrict__ flags,
     long long lhs, int lrs, int chs, int nB, int list_heads, unsigned bit_blocks, uint32_t* __restrict__ bits,
     uint32_t* __restrict__ part, const __nv_bfloat16* __restrict__ o, long long o_ts, long long o_hs,
     const __nv_bfloat16* __restrict__ go, const float* __restrict__ lse, int N, int H, float* __restrict__ nl,
-    float* __restrict__ nd) {
+    float* __restrict__ nd, bool ones, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+    const __nv_bfloat16* __restrict__ v, const BwdParams p) {
   constexpr int kWords = 256;
-  __shared__ uint32_t s_on[8][kWords], s_part[8][kWords];
+  constexpr int kThreads = prep_threads(FEW), kWarps = kThreads / 32;
+  __shared__ uint32_t s_on[kWarps][kWords], s_part[kWarps][kWords];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x < bit_blocks) {
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + warp;              // h * nB + query tile
+    const long long row = static_cast<long long>(blockIdx.x) * kWarps + warp;              // h * nB + query tile
     if (row >= static_cast<long long>(list_heads) * nB) return;
     const int h = static_cast<int>(row / nB), qb = static_cast<int>(row - static_cast<long long>(h) * nB);
     const int nW = (nB + 31) / 32;
@@ -173,28 +274,72 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(
   }
   constexpr int G = D / 8;
   const int NP = nB * 128;
-  const long long row = (static_cast<long long>(blockIdx.x - bit_blocks) * 256 + threadIdx.x) / G;   // n * H + h
+  const long long row = (static_cast<long long>(blockIdx.x - bit_blocks) * kThreads + threadIdx.x) / G;   // n * H + h
   const int l = threadIdx.x % G;
   const int n = static_cast<int>(row / H);
   const int h = static_cast<int>(row - static_cast<long long>(n) * H);
+  const bool on = n < N;
+  uint4 g = make_uint4(0u, 0u, 0u, 0u);
   float sum = 0.f;
-  if (n < N) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
-      sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
-    }
+  if (on) {
+    g = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
+    sum = dot8(__ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l)), g, 0.f);
   }
 #pragma unroll
   for (int s = G / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+  const float e = on ? lse[static_cast<size_t>(h) * N + n] : -INFINITY;
+  const float nle = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
+  bool one = false;
+  if constexpr (FEW) {
+    __shared__ int32_t s_keys[kThreads / G][kFewKeys];
+    const unsigned gm = ((1u << G) - 1u) << (lane & ~(G - 1));
+    int32_t* keys = s_keys[threadIdx.x / G];
+    const int t = on ? few_keys<G>(p, n, h, gm, l, keys) : 0;
+    if (t > 0) {
+      const uint4 qr = __ldg(reinterpret_cast<const uint4*>(q + row * D + 8 * l));
+      float all = 0.f, acc = 0.f;
+      constexpr int kBatch = 4;                     // keys in flight
+      for (int j0 = 0; j0 < t; j0 += kBatch) {
+        uint4 kr[kBatch], vr[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const size_t at = (static_cast<size_t>(keys[min(j0 + u, t - 1)]) * H + h) * D + 8 * l;
+          kr[u] = ld_pinned_v4(k + at);
+          vr[u] = ld_pinned_v4(v + at);
+        }
+        float s[kBatch], dp[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          s[u] = dot8(qr, kr[u], 0.f);
+          dp[u] = dot8(g, vr[u], 0.f);
+        }
+#pragma unroll
+        for (int i = G / 2; i > 0; i >>= 1) {
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            s[u] += __shfl_xor_sync(gm, s[u], i);
+            dp[u] += __shfl_xor_sync(gm, dp[u], i);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float pj = j0 + u < t ? ex2_approx(fmaf(s[u], p.sl2, nle)) : 0.f;
+          all += pj;
+          acc = fmaf(pj, dp[u], acc);
+        }
+      }
+      // only where o and lse are this list's: its probabilities sum to one
+      // (32-bit lse and exponentials move the sum by less than 2^-13)
+      if (fabsf(all - 1.f) <= 1.f / 4096) {
+        sum = acc / all;
+        one = ones && t == 1;
+      }
+    }
+  }
   if (l == 0 && n < NP) {
     const size_t at = static_cast<size_t>(h) * NP + n;
-    const float e = n < N ? lse[static_cast<size_t>(h) * N + n] : -INFINITY;
-    nl[at] = (e == -INFINITY) ? -INFINITY : -e * 1.4426950408889634f;
-    nd[at] = -sum;
+    nl[at] = nle;
+    nd[at] = one ? __uint_as_float(kOneKey) : -sum;
   }
 }
 
@@ -223,31 +368,6 @@ __device__ __forceinline__ int32_t ld_entry(const int32_t* p) {
   int32_t v;
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
-}
-
-__device__ __forceinline__ uint32_t bits32(int a, int b) {          // bits a .. b - 1, 0 <= a < b <= 32
-  return (b - a == 32 ? 0xFFFFFFFFu : (1u << (b - a)) - 1u) << a;
-}
-__device__ __forceinline__ bool frame_bit(const BwdParams& p, int fq, int fk) {
-  return (__ldg(p.fbits + static_cast<size_t>(fq) * p.TW + (fk >> 5)) >> (fk & 31)) & 1u;
-}
-// Element mask of 32 query columns for key frame fk: bit c set iff query q0+c
-// < N may attend it.
-__device__ __forceinline__ uint32_t query_mask(const BwdParams& p, int fk, int q0) {
-  uint32_t m = 0u;
-  const int qend = min(q0 + kBwdCols, p.N);
-  for (int f = q0 / p.P; f * p.P < qend; ++f)
-    if (frame_bit(p, f, fk)) m |= bits32(max(f * p.P, q0) - q0, min((f + 1) * p.P, qend) - q0);
-  return m;
-}
-// Element mask of 32 key columns for query frame fq (no frames: every key < N).
-__device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0) {
-  uint32_t m = 0u;
-  const int kend = min(k0 + kBwdCols, p.N);
-  if (p.fbits == nullptr) return k0 < kend ? bits32(0, kend - k0) : 0u;
-  for (int f = k0 / p.P; f * p.P < kend; ++f)
-    if (frame_bit(p, fq, f)) m |= bits32(max(f * p.P, k0) - k0, min((f + 1) * p.P, kend) - k0);
-  return m;
 }
 
 // COLS columns of one row of an f32 accumulator (TMEM) to bf16 in a
@@ -307,7 +427,7 @@ enum : int {
 static_assert(W_COUNT <= 32, "barrier slots");
 
 // dK and dV of key tile kt of head h.
-template <int D>
+template <int D, bool ONE>
 __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                         const CUtensorMap& tmG, const CUtensorMap& tmDK, const CUtensorMap& tmDV,
                                         const BwdParams& p, const int kt, const int h) {
@@ -516,6 +636,12 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
         const float4 nd = ld_shared_f4(rowv + 512 + 4 * c);
         f2unpack(fadd2(f2pack(dv[c], dv[c + 1]), f2pack(nd.x, nd.y)), dv[c], dv[c + 1]);
         f2unpack(fadd2(f2pack(dv[c + 2], dv[c + 3]), f2pack(nd.z, nd.w)), dv[c + 2], dv[c + 3]);
+        if constexpr (ONE) {
+          if (__float_as_uint(nd.x) == kOneKey) dv[c] = 0.f;
+          if (__float_as_uint(nd.y) == kOneKey) dv[c + 1] = 0.f;
+          if (__float_as_uint(nd.z) == kOneKey) dv[c + 2] = 0.f;
+          if (__float_as_uint(nd.w) == kOneKey) dv[c + 3] = 0.f;
+        }
       }
       tmem_st_x16(tDP, pk);
       tc_fence_before();
@@ -574,7 +700,7 @@ enum : int {
 };
 
 // dQ of query tile qt of head h.
-template <int D>
+template <int D, bool ONE>
 __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        const CUtensorMap& tmG, const CUtensorMap& tmDQ, const BwdParams& p,
                                        const int qt, const int h) {
@@ -765,6 +891,11 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
         f2unpack(fmul2(f2pack(pv[c], pv[c + 1]), fadd2(f2pack(dv[c], dv[c + 1]), ndp)), y0, y1);
         pk[c / 2] = pack_bf16x2(y0, y1);
       }
+      if constexpr (ONE) {
+        const bool one = __float_as_uint(nd) == kOneKey;
+#pragma unroll
+        for (int c = 0; c < kBwdCols / 2; ++c) pk[c] = one ? 0u : pk[c];
+      }
       tmem_st_x16(tS, pk);
       tc_fence_before();
       __syncwarp();
@@ -807,7 +938,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
 // The second order where the blocks fill the SMs only a few times (see
 // launch_bwd): 45.0 against 49.3 us for 208 blocks (26 tiles, 4 heads, d = 64),
 // but 2,466 against 2,409 us for 6,144 blocks (256 tiles, 12 heads, d = 128).
-template <int D>
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
@@ -815,9 +946,9 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const __grid_constant__ CUtensorMap tmDV, const BwdParams p) {
   const int t = blockIdx.x + blockIdx.z * p.nB, h = blockIdx.y;
   if (t < p.nB)
-    bwd_dkv<D>(tmQ, tmK, tmV, tmG, tmDK, tmDV, p, t, h);
+    bwd_dkv<D, ONE>(tmQ, tmK, tmV, tmG, tmDK, tmDV, p, t, h);
   else
-    bwd_dq<D>(tmQ, tmK, tmV, tmG, tmDQ, p, t - p.nB, h);
+    bwd_dq<D, ONE>(tmQ, tmK, tmV, tmG, tmDQ, p, t - p.nB, h);
 }
 
 }  // namespace bsa

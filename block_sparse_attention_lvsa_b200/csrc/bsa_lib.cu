@@ -947,11 +947,11 @@ int blockmean_select(const void* q, const void* k, int N, int H, int d, int bloc
 // Gradient of the block-sparse attention.
 namespace {
 
-template <int D>
+template <int D, bool ONE>
 int launch_bwd(const void* go, const void* q, const void* k, const void* v, int N, int H, const BwdParams& p,
                void* dq, void* dk, void* dv, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  const int rc = allow_smem(attn_bwd_kernel<D>, static_cast<int>(BwdSmem<D>::kAlloc), done);
+  const int rc = allow_smem(attn_bwd_kernel<D, ONE>, static_cast<int>(BwdSmem<D>::kAlloc), done);
   if (rc != BSA_OK) return rc;
   CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
   if (!make_qkv_map(&mq, q, N, H, D, 128) || !make_qkv_map(&mk, k, N, H, D, 128) ||
@@ -962,7 +962,7 @@ int launch_bwd(const void* go, const void* q, const void* k, const void* v, int 
   // all key tiles first where the blocks fill the SMs fewer than eight times
   const bool apart = 2LL * p.nB * H < 8 * 148;
   const dim3 grid(apart ? p.nB : 2 * p.nB, H, apart ? 2 : 1);
-  attn_bwd_kernel<D><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, mdk, mdv, p);
+  attn_bwd_kernel<D, ONE><<<grid, kBwdThreads, BwdSmem<D>::kAlloc, st>>>(mq, mk, mv, mg, mdq, mdk, mdv, p);
   return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -1036,15 +1036,25 @@ extern "C" int blocksparse_attn_bwd(const void* go, const void* q, const void* k
   p.part = part;
   p.bhs = w.lists == 1 ? 0 : static_cast<long long>((nB + 31) / 32) * nB;
   p.tlist = reinterpret_cast<int32_t*>(ws + w.tlist);
-  const unsigned bit_blocks = static_cast<unsigned>((static_cast<long long>(w.lists) * nB + 7) / 8);
-  const long long lanes = static_cast<long long>(nB) * 128 * H * (d / 8);
-  const unsigned blocks = bit_blocks + static_cast<unsigned>((lanes + 255) / 256);
   const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o->data);
   const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(go);
-  auto* prep = d == 128 ? attn_bwd_prep_kernel<128> : attn_bwd_prep_kernel<64>;
-  prep<<<blocks, 256, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB, w.lists, bit_blocks, bits, part, ob,
-                               o->token_stride, o->head_stride, gb, lse, N, H, nl, nd);
+  // Whether a row can have as few keys as kFewKeys, or one: whole frames have P
+  // each, listed blocks 128, but the last one what is left.
+  const int last = N - 128 * (nB - 1);
+  const int least = index->kind == BSA_INDEX_LVSA_FRAMES ? a.P : a.fbits != nullptr ? std::min(a.P, last) : last;
+  const bool ones = least == 1;
+  const bool few = index->kind == BSA_INDEX_LVSA_BLOCKS || least <= kFewKeys;   // parts of frames in blocks: any number
+  const int threads = prep_threads(few), warps = threads / 32;
+  const unsigned bit_blocks = static_cast<unsigned>((static_cast<long long>(w.lists) * nB + warps - 1) / warps);
+  const long long lanes = static_cast<long long>(nB) * 128 * H * (d / 8);
+  const unsigned blocks = bit_blocks + static_cast<unsigned>((lanes + threads - 1) / threads);
+  auto* prep = d == 128 ? (few ? attn_bwd_prep_kernel<128, true> : attn_bwd_prep_kernel<128, false>)
+                        : (few ? attn_bwd_prep_kernel<64, true> : attn_bwd_prep_kernel<64, false>);
+  prep<<<blocks, threads, 0, st>>>(a.list, a.count, a.flags, a.lhs, a.lrs, a.chs, nB, w.lists, bit_blocks, bits, part, ob,
+                               o->token_stride, o->head_stride, gb, lse, N, H, nl, nd, ones, static_cast<const __nv_bfloat16*>(q),
+                               static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), p);
   if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-  return d == 128 ? launch_bwd<128>(go, q, k, v, N, H, p, dq, dk, dv, st)
-                  : launch_bwd<64>(go, q, k, v, N, H, p, dq, dk, dv, st);
+  auto* launch = d == 128 ? (ones ? launch_bwd<128, true> : launch_bwd<128, false>)
+                          : (ones ? launch_bwd<64, true> : launch_bwd<64, false>);
+  return launch(go, q, k, v, N, H, p, dq, dk, dv, st);
 }

@@ -406,3 +406,136 @@ def test_chain_of_all_operators(bsa):
     for got, want in [(o, out), (dx, X.grad), (dwq, W[0].grad), (dwk, W[1].grad)]:
         rel = float((got.double() - want.detach()).norm() / want.detach().norm())
         assert rel <= 7 ** 0.5 * HALF, rel
+
+
+def compare_few(grads, go, q, k, v, scale, mask, what):
+    """As `compare`, for rows of at most 32 keys, whose D is not formed from the
+    rounded o: eD = 2^-13 sum p |dp| for its p; and the 32-bit sums over d
+    channels, each addition off by at most a step of 2^-23 of the magnitudes:
+    d 2^-23 <= 2^-16 of <|go|, |v|> in dp, and of its mean in D."""
+    go, q, k, v = map(f64, (go, q, k, v))
+    assert mask.sum(-1).max() <= 32
+    want = obwd.attention_back(go, q, k, v, scale, mask)
+    for h in range(q.shape[1]):
+        p = obwd.probabilities(q[:, h], k[:, h], scale, mask if mask.ndim == 2 else mask[h])
+        g, vh = go[:, h], v[:, h]
+        dp, size = g @ vh.T, 2.0 ** -16 * np.abs(g) @ np.abs(vh).T
+        D = (p * dp).sum(1, keepdims=True)
+        eD = (p * (2 * P32 * np.abs(dp) + size)).sum(1, keepdims=True)
+        eds = HALF * np.abs(p * (dp - D)) + p * (P32 * (np.abs(dp) + np.abs(D)) + size + eD)
+        bounds = (scale * eds @ np.abs(k[:, h]), scale * eds.T @ np.abs(q[:, h]), (HALF + P32) * p.T @ np.abs(g))
+        for name, got, ref, b in zip(("dq", "dk", "dv"), grads, want, bounds):
+            err = np.abs(f64(got)[:, h] - ref[:, h])
+            bound = b * (1 + HALF) + HALF * np.abs(ref[:, h]) + 1e-30
+            assert np.all(err <= bound), f"{what} {name} h={h}: worst err/bound {(err / bound).max()}"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 7, 31, 32])
+def test_few_keys(bsa, N, d):
+    idx, cnt = torch.zeros((2, 1, 1), dtype=torch.int32, device="cuda"), torch.ones((2, 1), dtype=torch.int32, device="cuda")
+    for seed in range(4):
+        go, q, k, v = make(N, 2, d, seed=200 + 10 * seed)
+        _, _, grads = both(bsa, go, q, k, v, bsa.block_index(idx, cnt))
+        assert bsa.get_device_status() == bsa.BSA_OK
+        compare_few(grads, go, q, k, v, d ** -0.5, np.ones((N, N), dtype=bool), f"N={N}")
+        if N == 1:                                          # p = 1: nothing that q or k could change
+            assert not grads[0].any() and not grads[1].any() and torch.equal(grads[2], go)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_key_or_many(bsa, d):
+    """Query block 0 sees the single key of the last block, block 1 that and a whole block, the last block itself."""
+    N, H = 2 * 128 + 1, 2
+    go, q, k, v = make(N, H, d, seed=240)
+    idx = torch.tensor([[2, -1, -1], [0, 2, -1], [2, -1, -1]], dtype=torch.int32, device="cuda").expand(H, 3, 3).contiguous()
+    cnt = torch.tensor([1, 2, 1], dtype=torch.int32, device="cuda").expand(H, 3).contiguous()
+    _, _, grads = both(bsa, go, q, k, v, bsa.block_index(idx, cnt))
+    assert bsa.get_device_status() == bsa.BSA_OK
+    compare(grads, go, q, k, v, d ** -0.5, block_mask(idx, cnt, N), "one key or many")
+    dq = grads[0]
+    assert not dq[:128].any() and dq[128:256].any() and not dq[256:].any()
+    cnt[:, 1] = 0                                           # only rows of one key and of none
+    _, _, (dq, dk, dv) = both(bsa, go, q, k, v, bsa.block_index(idx, cnt))
+    assert bsa.get_device_status() == bsa.BSA_OK
+    assert not dq.any() and not dk.any() and not dv[:256].any() and dv[256].any()
+
+
+@pytest.mark.parametrize("tail", [3, 32])
+def test_few_keys_of_a_short_last_block(bsa, tail):
+    """All queries but those of one block see the last block's keys, that block none."""
+    N, H, d = 3 * 128 + tail, 2, 64
+    go, q, k, v = make(N, H, d, seed=250)
+    idx = torch.full((H, 4, 4), -1, dtype=torch.int32, device="cuda")
+    cnt = torch.ones((H, 4), dtype=torch.int32, device="cuda")
+    idx[:, :, 0] = 3
+    cnt[:, 1] = 0
+    _, _, grads = both(bsa, go, q, k, v, bsa.block_index(idx, cnt))
+    assert bsa.get_device_status() == bsa.BSA_OK
+    compare_few(grads, go, q, k, v, d ** -0.5, block_mask(idx, cnt, N), "last block")
+
+
+@pytest.mark.parametrize("T,P,C,d", [(21, 1, 1, 64), (300, 1, 2, 128), (200, 3, 4, 64), (40, 16, 2, 128), (140, 32, 1, 64)])
+def test_few_keys_of_short_frames(bsa, T, P, C, d):
+    """The C frames of every row far apart: keys of several partial tiles."""
+    H, N = 2, T * P
+    go, q, k, v = make(N, H, d, seed=260 + T)
+    A = [sorted({(t + i * (T // C + 7)) % T for i in range(C)}) for t in range(T)]
+    frames = torch.full((T, T), -1, dtype=torch.int32)
+    for t, a in enumerate(A):
+        frames[t, :len(a)] = torch.tensor(a, dtype=torch.int32)
+    counts = torch.tensor([len(a) for a in A], dtype=torch.int32)
+    _, _, grads = both(bsa, go, q, k, v, bsa.lvsa_index(T, frames.cuda(), counts.cuda()))
+    assert bsa.get_device_status() == bsa.BSA_OK
+    compare_few(grads, go, q, k, v, d ** -0.5, olvsa.dense_token_mask(A, P, N), f"T={T} P={P}")
+    if P * C == 1:
+        assert not grads[0].any() and not grads[1].any()
+
+
+def test_few_keys_of_frames_within_blocks(bsa):
+    """Frames of 40 tokens, own frame and own block only: rows with 1 to 40 keys,
+    the ones in question where frames cross a block's border."""
+    T, P, H, d = 13, 40, 2, 128
+    N = T * P
+    go, q, k, v = make(N, H, d, seed=270)
+    frames = torch.full((T, T), -1, dtype=torch.int32)
+    frames[:, 0] = torch.arange(T, dtype=torch.int32)
+    nB = -(-N // 128)
+    idx = torch.full((H, nB, nB), -1, dtype=torch.int32, device="cuda")
+    idx[:, :, 0] = torch.arange(nB, device="cuda")
+    cnt = torch.ones((H, nB), dtype=torch.int32, device="cuda")
+    ix = bsa.lvsa_block_index(T, frames.cuda(), torch.ones(T, dtype=torch.int32, device="cuda"), idx, cnt)
+    _, _, grads = both(bsa, go, q, k, v, ix)
+    assert bsa.get_device_status() == bsa.BSA_OK
+    mask = olvsa.dense_token_mask([[t] for t in range(T)], P, N)[None] & block_mask(idx, cnt, N)
+    compare(grads, go, q, k, v, d ** -0.5, mask, "all rows")
+    few = np.flatnonzero(mask[0].sum(1) <= 32)              # whole groups: a frame's part in a block sees itself
+    assert 0 < len(few) < N
+    at = torch.from_numpy(few).cuda()
+    compare_few([x[at] for x in grads], go[at], q[at], k[at], v[at], d ** -0.5, mask[:, few][:, :, few], "few")
+
+
+def test_lists_that_split_the_keys(bsa):
+    """With o and lse of all keys, the gradients of lists that split the keys add
+    up, also where one of the lists has few keys: its D is the whole row's."""
+    N, H, d = 128 + 4, 2, 64
+    go, q, k, v = make(N, H, d, seed=280)
+    full = torch.tensor([0, 1], dtype=torch.int32, device="cuda").expand(H, 2, 2).contiguous()
+    two, one = (torch.full((H, 2), n, dtype=torch.int32, device="cuda") for n in (2, 1))
+    o, lse = bsa.blocksparse_attn_fwd(q, k, v, bsa.block_index(full, two))
+    parts = []
+    for b in range(2):
+        idx = torch.full((H, 2, 2), -1, dtype=torch.int32, device="cuda")
+        idx[:, :, 0] = b
+        parts.append(bsa.blocksparse_attn_bwd(go, q, k, v, o, lse, bsa.block_index(idx, one)))
+    assert bsa.get_device_status() == bsa.BSA_OK
+    for i in (1, 2):                                        # every key is in one of the lists
+        assert bool((parts[0][i][128:] == 0).all()) and bool((parts[1][i][:128] == 0).all())
+    # dq is rounded twice: within half a step of either part; kept in 32 bits, its
+    # sum is compared in `compare` as one rounding of |a + b|, so the rest is added there
+    dk, dv = (parts[0][i] + parts[1][i] for i in (1, 2))
+    dq = obwd.attention_back(*map(f64, (go, q, k, v)), d ** -0.5, np.ones((N, N), dtype=bool))[0]
+    compare((torch.from_numpy(dq), dk, dv), go, q, k, v, d ** -0.5, np.ones((N, N), dtype=bool), "split")
+    a, b = f64(parts[0][0]), f64(parts[1][0])
+    whole = f64(bsa.blocksparse_attn_bwd(go, q, k, v, o, lse, bsa.block_index(full, two))[0])
+    assert np.linalg.norm(a + b - whole) <= HALF * (np.linalg.norm(a) + np.linalg.norm(b) + np.linalg.norm(whole))

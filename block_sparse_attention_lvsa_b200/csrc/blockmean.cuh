@@ -56,8 +56,10 @@ struct PoolSmem {
 // always give equal means.
 // 225 us under ncu for q and k of 196560 x 12 x 128 (1.21 GB, 5.4 TB/s); the unit
 // that converts to 64 bits is 69% busy.  Loads and adds in the same warps: 272 us;
-// half of the conversions by moving bits in the integer pipe: 246 us; four
-// adding warps with twice the tokens each: 285 us.
+// half of the conversions by moving bits in the integer pipe: 246 us; half of
+// them by adding two tokens in 32 bits first, where that is exact: 226 us; four
+// adding warps with twice the tokens each: 285 us; two or four blocks an SM: the
+// whole call 9 to 14 us slower.
 // mean: [2][H][nB][d] double; hi, lo: bf16 [2][H][nB][d]; norm: [2][H][nB] double.
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel(
     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel
     const int slab = static_cast<int>(t % slabs);
     const int zb = static_cast<int>(t / slabs), z = zb >= nB, b = zb - z * nB;
     const int rows = min(128, N - b * 128);
-    double acc[8];                                    // odd channels times 2^-896
+    double acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0;
 #pragma unroll 1
@@ -123,8 +125,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtas) blockmean_pool_kernel
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v[i] = *reinterpret_cast<const uint4*>(gbase + slot * L::kStage + (warp * 4 + i) * 512 + lane * 16);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(slot));
+      mbar_arrive_after(empty(slot), v[0].x | v[1].x | v[2].x | v[3].x, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};

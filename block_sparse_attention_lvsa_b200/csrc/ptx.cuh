@@ -41,6 +41,15 @@ __device__ __forceinline__ void fence_mbar_init() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// One arrival of the calling warp that shared memory it has read may be written
+// again.  `loaded` combines (by or) a word of each load: the arriving lane is
+// found from it, so the arrival cannot come before the loads' data have.  Behind
+// the loads alone an arrival does not wait for them: with their use moved down
+// (32 conversions between) the next TMA box overwrote what was still to be read.
+__device__ __forceinline__ void mbar_arrive_after(uint32_t bar, uint32_t loaded, int lane) {
+  const uint32_t votes = __ballot_sync(0xFFFFFFFFu, loaded != 0u) | 0x80000000u;
+  if (lane == __ffs(votes) - 1) mbar_arrive(bar);
+}
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");

@@ -213,3 +213,18 @@ def test_over_budget_is_a_warning(bsa):
     assert cnt[0].tolist() == [2, 3, 3, 3, 3, 3, 3, 2]
     assert call(3, 1) == bsa.BSA_OK
     assert call(100, 10 ** 9) == bsa.BSA_OK and cnt[0].tolist() == [8] * 8
+
+
+@pytest.mark.parametrize("N,H,d", [(128 * 1537, 1, 64), (128 * 700 - 5, 2, 64), (128 * 300, 3, 128)])
+def test_repeated_calls_agree(bsa, N, H, d):
+    """q and k in L2, where the pooling's loads are fastest: a box of its ring that
+    is written again too early would change means, and with them the choice."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    q, k = (torch.randn((N, H, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    nB = -(-N // 128)
+    first = bsa.blockmean_select(q, k, nB // 3, 1)
+    idx, cnt = (torch.empty_like(x) for x in first)
+    for _ in range(60):
+        bsa.blockmean_select(q, k, nB // 3, 1, idx=idx, cnt=cnt)
+        assert torch.equal(idx, first[0]) and torch.equal(cnt, first[1])
+    assert bsa.get_device_status() == bsa.BSA_OK

@@ -120,3 +120,14 @@ def test_binding_refuses_cpu_and_wrong_tensors(bsa):
         bsa.rope_axes([torch.zeros((4, 8, 2))], grid=(4,), pairing="interleaved")
     with pytest.raises(ValueError):
         bsa.rope_build_table(0, 4, device="cuda:0")
+
+
+def test_packed_rope_fills_the_struct_field_by_field(bsa):
+    """The one-call packing puts every value where the struct has its field."""
+    assert bsa._ROPE.size == ctypes.sizeof(bsa.bsa_rope)
+    r = bsa.bsa_rope.from_buffer_copy(bsa._ROPE.pack(*range(1, 18)))
+    seen = []
+    for name, kind in bsa.bsa_rope._fields_:
+        v = getattr(r, name)
+        seen += list(v) if issubclass(kind, ctypes.Array) else [v]
+    assert seen == list(range(1, 18))

@@ -147,14 +147,24 @@ __device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0)
 // can all be small: dq and dk of 2 tokens were off by up to 6e-2 of their norm.
 // Up to kFewKeys keys D is therefore formed anew in 32 bits,
 //   D = sum p <do, v_k> / sum p,
-// from which the sum of ds over the row vanishes as it should.  The rounding of
-// o averages out over the keys: with 32 or more it adds less to the error of
-// the gradients (3.1e-3 to 3.6e-3 of their norm with 16 keys, 2.6e-3 to 3.0e-3
-// with 64) than the rounding of p and ds (2.4e-3).  A row of one key has p = 1
-// and ds = 0 whatever dP is; where such rows can fill the input (`ones`: frames
-// of one token, a last block of one key) they get the mark kOneKey in place of
-// -D, a NaN that no arithmetic gives, at which ds is set to 0.  Elsewhere the
-// check would cost 5% (947 against 889 us, 161 blocks, 12 heads, d = 128).
+// from which the sum of ds over the row vanishes as it should, whatever factor
+// lse is off by (its 32 bits leave 2^-22 |lse| of the exponent: p of a row with
+// scores near 8,000 sums to 1 only within 4e-3).  The rounding of o averages out
+// over the keys: with 32 or more it adds less to the error of the gradients
+// (3.1e-3 to 3.6e-3 of their norm with 16 keys, 2.6e-3 to 3.0e-3 with 64) than
+// the rounding of p and ds (2.4e-3).
+// That D is right only where o and lse are of this list, not of one with more
+// keys.  They are taken to be where it is as near to <do, o> as o's rounding and
+// that of the forward's p leave it,
+//   |D - <do, o>| <= 2^-8 (<|do|, |o|> + sum p <|do|, |v_k|>)
+// (and an eighth more for the 32-bit sums): rows of the forward's own list meet
+// that at scores of any size, and where another row meets it the one D is as good
+// as the other.
+// A row of one key has p = 1 and ds = 0 whatever dP is; where such rows can fill
+// the input (`ones`: frames of one token, a last block of one key) they get the
+// mark kOneKey in place of -D, a NaN that no arithmetic gives, at which ds is set
+// to 0.  Elsewhere the check would cost 5% (947 against 889 us, 161 blocks, 12
+// heads, d = 128).
 constexpr int kFewKeys = 32;
 constexpr uint32_t kOneKey = 0x7FC00001u;
 // What it costs the whole gradient: 10.6 -> 16.6 us where every row has 32 keys
@@ -204,6 +214,18 @@ __device__ __forceinline__ uint4 ld_pinned_v4(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+constexpr float kRoundedO = 1.125f / 256.f;        // 2^-8 and an eighth
+// <|x|, |y|> over 8 channels in bf16
+__device__ __forceinline__ float abs_dot8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fmaf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(y[i] << 16)), sum);
+    sum = fmaf(fabsf(__uint_as_float(x[i] & 0xFFFF0000u)), fabsf(__uint_as_float(y[i] & 0xFFFF0000u)), sum);
+  }
+  return sum;
 }
 // <x, y> over 8 channels in bf16
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
@@ -280,10 +302,12 @@ __global__ void __launch_bounds__(prep_threads(FEW)) attn_bwd_prep_kernel(
   const int h = static_cast<int>(row - static_cast<long long>(n) * H);
   const bool on = n < N;
   uint4 g = make_uint4(0u, 0u, 0u, 0u);
-  float sum = 0.f;
+  float sum = 0.f, size = 0.f;                        // size: <|do|, |o|> + sum p <|do|, |v_k|>, of the lane's channels
   if (on) {
     g = __ldg(reinterpret_cast<const uint4*>(go + row * D + 8 * l));
-    sum = dot8(__ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l)), g, 0.f);
+    const uint4 ov = __ldg(reinterpret_cast<const uint4*>(o + n * o_ts + h * o_hs + 8 * l));
+    sum = dot8(ov, g, 0.f);
+    if (FEW) size = abs_dot8(ov, g);
   }
 #pragma unroll
   for (int s = G / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
@@ -307,11 +331,12 @@ __global__ void __launch_bounds__(prep_threads(FEW)) attn_bwd_prep_kernel(
           kr[u] = ld_pinned_v4(k + at);
           vr[u] = ld_pinned_v4(v + at);
         }
-        float s[kBatch], dp[kBatch];
+        float s[kBatch], dp[kBatch], sz[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           s[u] = dot8(qr, kr[u], 0.f);
           dp[u] = dot8(g, vr[u], 0.f);
+          sz[u] = abs_dot8(g, vr[u]);
         }
 #pragma unroll
         for (int i = G / 2; i > 0; i >>= 1) {
@@ -326,12 +351,14 @@ __global__ void __launch_bounds__(prep_threads(FEW)) attn_bwd_prep_kernel(
           const float pj = j0 + u < t ? ex2_approx(fmaf(s[u], p.sl2, nle)) : 0.f;
           all += pj;
           acc = fmaf(pj, dp[u], acc);
+          size = fmaf(pj, sz[u], size);
         }
       }
-      // only where o and lse are this list's: its probabilities sum to one
-      // (32-bit lse and exponentials move the sum by less than 2^-13)
-      if (fabsf(all - 1.f) <= 1.f / 4096) {
-        sum = acc / all;
+#pragma unroll
+      for (int i = G / 2; i > 0; i >>= 1) size += __shfl_xor_sync(gm, size, i);
+      const float own = acc / all;                    // no key of any weight: not a number, not taken
+      if (fabsf(own - sum) <= kRoundedO * size) {
+        sum = own;
         one = ones && t == 1;
       }
     }

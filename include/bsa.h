@@ -341,8 +341,11 @@ typedef struct bsa_heads {
  *   dv_k = sum_q p go_q,   ds = p (<go_q, v_k> - D_q),
  *   dq_q = scale sum_k ds k_k,   dk_k = scale sum_q ds q_q.
  * Sums in float32, the factors p and ds of the products and the outputs
- * rounded to bfloat16; for rows of at most 32 keys D_q is formed as
- * sum_k p <go_q, v_k>, free of the rounding of o.  No atomics: the result is the same from run to run.
+ * rounded to bfloat16.  For rows of at most 32 keys D_q is formed as
+ * sum_k p <go_q, v_k> / sum_k p, free of the rounding of o, where that is within
+ * the rounding of o from <go_q, o_q> (it is when o and lse are the forward's for
+ * this index); a row of one key then has ds = 0.  No atomics: the result is the
+ * same from run to run.
  * Queries without a key, and keys that no query attends, get 0.
  *
  * go, q, k, v: in, bf16 [N,H,d]; o: in, bf16 [N,H,d] by strides (a saved o may

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <numeric>
 
 #include "ptx.cuh"
 #include "lvsa_index.cuh"
@@ -523,6 +524,50 @@ int check_heads(const bsa_heads* t, int dtype, long long N, int d, bool out) {
   return BSA_OK;
 }
 
+// Whether two tensors share memory: for tokens the same stride apart in both (as
+// slices of one projection are) the exact answer; with token strides of their own,
+// or more than 2^20 pairs of heads to go through, any common range counts.
+bool share_memory(const bsa_heads* a, const bsa_heads* b, int dtype, long long N, int d) {
+  const long long ats = N > 1 ? a->token_stride : 0, bts = N > 1 ? b->token_stride : 0;
+  const long long ahs = a->H > 1 ? a->head_stride : 0, bhs = b->H > 1 ? b->head_stride : 0;
+  const long long aw = (a->H - 1) * ahs + d, bw = (b->H - 1) * bhs + d;         // a token's range
+  const long long diff = (reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data)) / esize(dtype);
+  if (diff >= (N - 1) * ats + aw || -diff >= (N - 1) * bts + bw) return false;
+  if (ats != bts) return true;
+  auto apart = [&](long long period, long long wa, long long wb) {              // modulo `period`
+    if (period == 0) return false;
+    const long long r = (diff % period + period) % period;
+    return r >= wa && r + wb <= period;
+  };
+  if (apart(ats, aw, bw) || apart(std::gcd(std::gcd(ats, ahs), bhs), d, d)) return false;
+  // rows h of a and g of b meet where |x + n ats| < d for a number n of tokens between them
+  auto meet = [&](long long x) {
+    if (ats == 0) return -d < x && x < d;
+    auto floor_div = [&](long long y) { return y / ats - (y % ats < 0 ? 1 : 0); };
+    return std::max(-floor_div(x + d - 1), 1 - N) <= std::min(floor_div(d - 1 - x), N - 1);
+  };
+  if (ahs == bhs || a->H == 1 || b->H == 1) {
+    const long long hs = std::max(ahs, bhs);
+    for (long long h = 1 - a->H; h < b->H; ++h)
+      if (meet(diff + h * hs)) return true;
+    return false;
+  }
+  if (static_cast<long long>(a->H) * b->H > (1 << 20)) return true;
+  for (long long h = 0; h < a->H; ++h)
+    for (long long g = 0; g < b->H; ++g)
+      if (meet(diff + g * bhs - h * ahs)) return true;
+  return false;
+}
+
+// An output next to a tensor that it may replace (its own input or gradient, with
+// the same layout) or, without `own`, to any other.
+bool in_the_way(const bsa_heads* out, const bsa_heads* t, int dtype, long long N, int d, bool own) {
+  if (own && out->data == t->data && out->H == t->H && (N == 1 || out->token_stride == t->token_stride) &&
+      (t->H == 1 || out->head_stride == t->head_stride))
+    return false;
+  return share_memory(out, t, dtype, N, d);
+}
+
 int check_sizes(int dtype, long long N, int d) {
   if (dtype != BSA_BF16 && dtype != BSA_F16 && dtype != BSA_F32) return BSA_ERR_ARG;
   if (N < 1) return BSA_ERR_ARG;
@@ -704,6 +749,7 @@ int rope_apply(const bsa_heads* x, const bsa_heads* y, int dtype, long long N, i
   std::memset(&p, 0, sizeof(p));
   p.N = N;
   if ((rc = rope_dev(rope, N, d, inverse != 0, &p.r)) != BSA_OK) return rc;
+  if (in_the_way(y, x, dtype, N, d, true)) return BSA_ERR_ARG;
   set_tensor(&p.t[0], x, nullptr, y, nullptr);
   return launch_rope_fwd_any(p, dtype, d, 1, rope->pairing == BSA_ROPE_SPLIT, false,
                              static_cast<cudaStream_t>(stream));
@@ -730,6 +776,10 @@ int qk_norm_rope_fwd(const bsa_heads* q, const bsa_heads* k, const bsa_heads* qo
   p.eps = eps;
   p.w_f32 = wtype == BSA_F32;
   if ((rc = rope_dev(rope, N, d, false, &p.r)) != BSA_OK) return rc;
+  if (in_the_way(qo, q, dtype, N, d, true)) return BSA_ERR_ARG;
+  if (k && (in_the_way(ko, k, dtype, N, d, true) || in_the_way(qo, k, dtype, N, d, false) ||
+            in_the_way(ko, q, dtype, N, d, false) || in_the_way(qo, ko, dtype, N, d, false)))
+    return BSA_ERR_ARG;
   set_tensor(&p.t[0], q, nullptr, qo, wq);
   if (k) set_tensor(&p.t[1], k, nullptr, ko, wk);
   return launch_rope_fwd_any(p, dtype, d, tensors, rope && rope->pairing == BSA_ROPE_SPLIT, true,
@@ -773,6 +823,13 @@ int qk_norm_rope_bwd(const bsa_heads* gq, const bsa_heads* gk, const bsa_heads* 
   if (!workspace || !aligned(workspace, 256) ||
       ws_bytes < qk_norm_rope_bwd_workspace_bytes(N, q->H, k ? k->H : 0, d))
     return BSA_ERR_WORKSPACE;
+  for (const bsa_heads* t : {q, gq})
+    if (in_the_way(dq, t, dtype, N, d, true) || (k && in_the_way(dk, t, dtype, N, d, false))) return BSA_ERR_ARG;
+  if (k) {
+    for (const bsa_heads* t : {k, gk})
+      if (in_the_way(dk, t, dtype, N, d, true) || in_the_way(dq, t, dtype, N, d, false)) return BSA_ERR_ARG;
+    if (in_the_way(dq, dk, dtype, N, d, false)) return BSA_ERR_ARG;
+  }
   set_tensor(&p.t[0], q, gq, dq, wq);
   if (k) set_tensor(&p.t[1], k, gk, dk, wk);
   p.partial = static_cast<float*>(workspace);

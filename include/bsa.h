@@ -326,6 +326,11 @@ enum {
  * Strides of inputs are >= 0 (0 repeats the same row); the rows of an output
  * must not overlap one another: the smaller of the two strides is at least d
  * and the larger at least the smaller times its extent (H or N).
+ * A call that allows an output to be its own input takes the same data, strides
+ * and H for both; any other output that shares memory with an input or output of
+ * the call is refused with BSA_ERR_ARG.  Interleaved slices of one buffer (a
+ * packed projection) share none; tensors whose token strides differ must lie in
+ * separate ranges.
  */
 typedef struct bsa_heads {
   void* data;
@@ -448,7 +453,8 @@ int rope_build_table(int len, int pairs, double theta, double start, double step
  * and is its gradient.
  *
  * x: in; y: out, same H; y may be x itself (same data and strides), otherwise
- * the two must not overlap.  dtype: BSA_BF16, BSA_F16 or BSA_F32, of both.
+ * the two must not overlap (checked, see bsa_heads).  dtype: BSA_BF16, BSA_F16
+ * or BSA_F32, of both.
  * Returns BSA_OK or a negative bsa_status.
  */
 int rope_apply(const bsa_heads* x, const bsa_heads* y, int dtype, long long N, int d,
@@ -462,9 +468,10 @@ int rope_apply(const bsa_heads* x, const bsa_heads* y, int dtype, long long N, i
  * over the d channels of every (token, head), in float32, rounded once.
  *
  * q, k: in; qo, ko: out, same H as q and k (H of q and k may differ); an
- * output may be its own input, otherwise nothing may overlap.  k and ko may
- * both be NULL (queries alone).  wq, wk: device [d], 16-byte aligned, of type
- * wtype (BSA_F32 or the tensors' dtype), or NULL for a norm without weights.
+ * output may be its own input, otherwise nothing may overlap (checked, see
+ * bsa_heads).  k and ko may both be NULL (queries alone).  wq, wk: device [d],
+ * 16-byte aligned, of type wtype (BSA_F32 or the tensors' dtype), or NULL for a
+ * norm without weights.
  * eps: finite, > 0.  rope: NULL for the norm alone.
  * Returns BSA_OK or a negative bsa_status.
  */
@@ -477,10 +484,10 @@ int qk_norm_rope_fwd(const bsa_heads* q, const bsa_heads* k, const bsa_heads* qo
  *
  * gq, gk: in, gradients of qo and ko; q, k, wq, wk, eps, rope: as given to
  * the forward call.  dq, dk: out, gradients of q and k (dtype; each may be
- * its gq / gk or its q / k).  dwq, dwk: out, device float32 [d], gradients of
- * the weights, summed over tokens and heads in a fixed order (the same from
- * run to run); NULL where they are not wanted.  gk, k and dk may be NULL
- * together (then dwk must be NULL).
+ * its gq / gk or its q / k, and overlap nothing else: checked, see bsa_heads).
+ * dwq, dwk: out, device float32 [d], gradients of the weights, summed over
+ * tokens and heads in a fixed order (the same from run to run); NULL where they
+ * are not wanted.  gk, k and dk may be NULL together (then dwk must be NULL).
  * workspace: device, 256-byte aligned, at least
  * qk_norm_rope_bwd_workspace_bytes(N, H of q, H of k or 0, d) bytes;
  * overwritten.

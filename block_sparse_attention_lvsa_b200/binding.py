@@ -412,7 +412,10 @@ def losa_select(mass: torch.Tensor, tau: float = 0.99, idx=None, cnt=None, strea
 _DTYPES = {torch.bfloat16: BSA_BF16, torch.float16: BSA_F16, torch.float32: BSA_F32}
 _PAIRINGS = {"adjacent": BSA_ROPE_ADJACENT, "split": BSA_ROPE_SPLIT}
 _ROPE = struct.Struct("@i3i3i3P3i3iP")         # bsa_rope, packed in one go
-_raw_stream = torch._C._cuda_getCurrentRawStream       # handle of a device's current stream, without a Stream object
+# handle of a device's current stream, without a Stream object where torch's C module offers
+# that (it has no such name in builds without CUDA, where the host checks still serve)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _enter(device: torch.device, stream):

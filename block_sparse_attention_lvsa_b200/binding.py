@@ -675,10 +675,12 @@ def qk_norm_rope_bwd(gq: torch.Tensor, gk: Optional[torch.Tensor], q: torch.Tens
 
 # ------------------------------------------------ key blocks by block means ---
 def blockmean_select(q: torch.Tensor, k: torch.Tensor, keep: int, local: int = 0, block: int = 128, idx=None, cnt=None,
-                     workspace: Optional[torch.Tensor] = None, stream=None):
+                     workspace: Optional[torch.Tensor] = None, stream=None, return_over_budget: bool = False):
     """Per (head, query block) the ``keep`` key blocks of the largest mean score, the blocks
     within ``local`` of the own one always among them (-1: none forced); returns
-    (idx [H,nB,nB] int32 ascending, -1 padded, cnt [H,nB] int32) for block_index."""
+    (idx [H,nB,nB] int32 ascending, -1 padded, cnt [H,nB] int32) for block_index.
+    A neighbourhood of more than ``keep`` blocks is kept whole (cnt says so); with
+    ``return_over_budget`` a third value tells whether there is one."""
     _check_qkv(q, k, k)
     if k.device != q.device:
         raise ValueError(f"k must be on {q.device}, got {k.device}")
@@ -705,7 +707,7 @@ def blockmean_select(q: torch.Tensor, k: torch.Tensor, keep: int, local: int = 0
     finally:
         _leave(guard)
     _check("blockmean_select", rc, (BSA_OK, BSA_WARN_OVER_BUDGET))
-    return idx, cnt
+    return (idx, cnt, rc == BSA_WARN_OVER_BUDGET) if return_over_budget else (idx, cnt)
 
 
 # ------------------------------------------------- gradient of the attention ---

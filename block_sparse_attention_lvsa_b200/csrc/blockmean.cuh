@@ -8,24 +8,34 @@
 // 128 x 128.  Kept for row i: its own neighbourhood |i - j| <= local, then
 // the largest s, at equal scores the lower j first, up to `keep` blocks.
 //
-// A border between kept and dropped must not depend on rounding: the means and
-// the scores that decide are 64-bit.  64-bit scores of every tile would cost
-// far more than reading q and k (9.5 ms against 0.2 ms at 1536 blocks and 12
-// heads of 128), so they are taken only near the border:
+// The rounding of 32-bit sums must not decide between kept and dropped: the means
+// and the scores that decide are 64-bit, a score within 2^-49 |mean q| |mean k| of
+// the exact one (up to 4 products and 5 additions a lane and two means, half a
+// step of 2^-53 each).  Blocks of equal means have equal scores and go by their
+// index; blocks whose scores are closer than that without being the same may be
+// ordered by rounding.  64-bit scores of every tile would cost far more than
+// reading q and k (9.5 ms against 0.2 ms at 1536 blocks and 12 heads of 128), so
+// they are taken only near the border:
 //  1. blockmean_pool_kernel: means in 64 bits, split in two bf16 parts
 //     (m = hi + lo + rest, |rest| <= 2^-16 |m|), and their norms; one read of q
 //     and k, the HBM bound of the operator.
 //  2. blockmean_score_kernel: hi hi + hi lo + lo hi on the tensor cores, off by
 //     less than E = 2^-13 |mean q| max_j |mean k_j|: the parts leave out at most
 //     3 * 2^-16 sum |q_c k_c|, and 3 d <= 384 additions in 32 bits at most
-//     384 * 2^-23 of it, together 9.2e-5 < 2^-13 = 1.22e-4 of |q| |k|.
+//     384 * 2^-23 of it, together 9.2e-5 < 2^-13 = 1.22e-4 of |q| |k|.  (This
+//     takes the tensor cores to lose at most a step of 2^-23 of the magnitudes
+//     with each product that they add; measured, sums of 128 products of one sign
+//     are low by 2.8 * 2^-24 on average and 7.3 * 2^-24 at most.)
 //  3. blockmean_select_kernel: the take-th largest rough score t of a row is
 //     within E of the take-th largest exact one, so a block above t + 2E is
 //     kept, one below t - 2E is not, and only those between (a few of 1536)
-//     get 64-bit scores.  Rows whose norms leave the range where these bounds
-//     hold (32-bit products near the ends of the exponent, values that are not
-//     finite), and calls with so few blocks that there are no rough scores, get
-//     64-bit scores throughout.
+//     get 64-bit scores.  E grows with what all key blocks share, although that
+//     changes no ranking: the whole call takes 409 us for 12 heads of 1536 blocks
+//     of unrelated tokens, 427, 1,382 and 3,087 us where every key has a common
+//     part of norm 3, 10 and 30 (more than kSelKeys candidates: see below).
+//     Rows whose norms leave the range where these bounds hold (32-bit products
+//     near the ends of the exponent, values that are not finite), and calls with
+//     so few blocks that there are no rough scores, get 64-bit scores throughout.
 #pragma once
 #include "rope.cuh"   // packed pairs of float
 

@@ -384,7 +384,9 @@ int blocksparse_attn_bwd(const void* go, const void* q, const void* k, const voi
  * |i - j| <= local and then the blocks of the largest s, at equal scores the
  * lower j first, until it holds max(min(keep, nB), size of the neighbourhood)
  * blocks; the list is written ascending.  Means and deciding scores are
- * computed in 64 bits; a score that is not a number counts as the lowest.
+ * computed in 64 bits, within 2^-49 of |mean q| |mean k|: blocks of equal means
+ * have equal scores, scores closer than that may be ordered by rounding.  A score
+ * that is not a number counts as the lowest.
  * Unlike losa_select this needs no dense step: q and k are read once.
  *
  * q, k: in, bf16 [N,H,d].  block: must be 128.  keep >= 1.  local >= -1 (-1:

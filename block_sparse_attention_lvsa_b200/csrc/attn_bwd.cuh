@@ -158,8 +158,9 @@ __device__ __forceinline__ uint32_t key_mask(const BwdParams& p, int fq, int k0)
 // that of the forward's p leave it,
 //   |D - <do, o>| <= 2^-8 (<|do|, |o|> + sum p <|do|, |v_k|>)
 // (and an eighth more for the 32-bit sums): rows of the forward's own list meet
-// that at scores of any size, and where another row meets it the one D is as good
-// as the other.
+// that whatever the factor is (tested up to scores of 8,000), and where another
+// row meets it the one D is as good as the other.  The sum of p does not tell them
+// apart: with |sum p - 1| <= 2^-12 most rows at scores of 2,000 were missed.
 // A row of one key has p = 1 and ds = 0 whatever dP is; where such rows can fill
 // the input (`ones`: frames of one token, a last block of one key) they get the
 // mark kOneKey in place of -D, a NaN that no arithmetic gives, at which ds is set
